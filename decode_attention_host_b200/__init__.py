@@ -33,6 +33,8 @@ DKV_STATUS_BAD_BLOCK_ID = 1
 DKV_STATUS_BAD_SEQ_LEN = 2
 DKV_STATUS_COPY_TIMEOUT = 4
 DKV_STATUS_INTERNAL = 8
+DKV_STATUS_NO_FREE_BLOCKS = 16
+DKV_STATUS_NO_SLOTS = 32
 DKV_KV_F16 = 0
 DKV_KV_BF16 = 1
 DKV_PLACE_PREFIX_HOST = 0
@@ -43,7 +45,8 @@ EXPORTED = ("dkv_create", "dkv_destroy", "dkv_attn_decode", "dkv_get_status", "d
             "dkv_plan_blocks", "dkv_pack_kv", "dkv_profile_begin", "dkv_profile_end",
             "dkv_attn_decode_noalloc", "dkv_plan_offload", "dkv_attn_decode_staged", "dkv_append_kv",
             "dkv_attn_decode_multi", "dkv_debug_rope", "dkv_profile_timeline", "dkv_debug_fail_alloc",
-            "dkv_debug_stall_copy")
+            "dkv_debug_stall_copy", "dkv_extend_tables", "dkv_store_kv", "dkv_attn_chunk",
+            "dkv_attn_decode_window")
 
 
 class DkvConfig(ctypes.Structure):
@@ -103,6 +106,11 @@ def _load() -> ctypes.CDLL:
         "dkv_profile_timeline": [vp, i32, c.POINTER(c.c_float)],
         "dkv_debug_fail_alloc": [i32],
         "dkv_debug_stall_copy": [i32],
+        "dkv_extend_tables": [vp, vp, vp, i32, vp, i32, vp, i32, vp, vp, vp, vp, i32, vp],
+        "dkv_store_kv": [vp, vp, vp, i64, vp, i32, i32, vp, vp, vp, vp, vp, i32],
+        "dkv_attn_chunk": [vp, vp, i64, vp, i32, vp, vp, vp, vp, vp, vp, i32, vp, i32, i32, i32, vp, i32, i32, i32,
+                           vp, vp],
+        "dkv_attn_decode_window": [vp, i32, i32, i32, vp, vp, vp, vp, vp, vp, vp, i32, vp, vp, i32, i32, i32],
     }
     for name, args in sig.items():
         fn = getattr(lib, name)
@@ -168,6 +176,35 @@ def dkv_attn_decode_multi(h, num_queries, q, k_host, v_host, k_dev, v_dev, block
     _check(lib.dkv_attn_decode_multi(h, int(num_queries), _p(q), _p(k_host), _p(v_host), _p(k_dev), _p(v_dev),
                                      _p(block_table), _p(seq_lens), int(host_split), _p(out), stream, int(batch),
                                      int(block_table_stride), int(num_dev_blocks)))
+
+
+def dkv_extend_tables(h, seq_lens, new_lens, batch, block_table, block_table_stride, free_ids, free_capacity,
+                      free_count, free_left, q_start, slot_map, max_slots, stream) -> None:
+    _check(lib.dkv_extend_tables(h, _p(seq_lens), _p(new_lens), int(batch), _p(block_table), int(block_table_stride),
+                                 _p(free_ids), int(free_capacity), _p(free_count), _p(free_left), _p(q_start),
+                                 _p(slot_map), int(max_slots), stream))
+
+
+def dkv_store_kv(h, k_new, v_new, row_stride, slot_map, num_rows, host_split, k_host, v_host, k_dev, v_dev, stream,
+                 num_dev_blocks) -> None:
+    _check(lib.dkv_store_kv(h, _p(k_new), _p(v_new), int(row_stride), _p(slot_map), int(num_rows), int(host_split),
+                            _p(k_host), _p(v_host), _p(k_dev), _p(v_dev), stream, int(num_dev_blocks)))
+
+
+def dkv_attn_chunk(h, q, q_stride, q_start, total_rows, k_host, v_host, k_dev, v_dev, block_table, seq_lens,
+                   host_split, out, window, sinks, include_self, stream, batch, block_table_stride, num_dev_blocks,
+                   k_stage=None, v_stage=None) -> None:
+    _check(lib.dkv_attn_chunk(h, _p(q), int(q_stride), _p(q_start), int(total_rows), _p(k_host), _p(v_host),
+                              _p(k_dev), _p(v_dev), _p(block_table), _p(seq_lens), int(host_split), _p(out),
+                              int(window), int(sinks), int(include_self), stream, int(batch),
+                              int(block_table_stride), int(num_dev_blocks), _p(k_stage), _p(v_stage)))
+
+
+def dkv_attn_decode_window(h, window, sinks, include_self, q, k_host, v_host, k_dev, v_dev, block_table, seq_lens,
+                           host_split, out, stream, batch, block_table_stride, num_dev_blocks) -> None:
+    _check(lib.dkv_attn_decode_window(h, int(window), int(sinks), int(include_self), _p(q), _p(k_host), _p(v_host),
+                                      _p(k_dev), _p(v_dev), _p(block_table), _p(seq_lens), int(host_split), _p(out),
+                                      stream, int(batch), int(block_table_stride), int(num_dev_blocks)))
 
 
 def dkv_get_status(h: int) -> int:
@@ -394,6 +431,63 @@ class DecodeAttention:
                               kv.k_dev if kv.num_dev_blocks else None, kv.v_dev if kv.num_dev_blocks else None,
                               kv.table_dev, kv.seq_lens_dev, kv.host_split, out, stream.cuda_stream, kv.batch,
                               kv.stride, kv.num_dev_blocks)
+
+    def extend(self, kv: PagedKV, new_lens, free_ids, free_count, max_slots: int, stream=None):
+        """Blocks and slots for new_lens[b] more tokens of every sequence (device int32 tensors): returns
+        (q_start, slot_map); kv's table grows and free_count goes down in place, kv.seq_lens_dev stays."""
+        import torch
+        dev = new_lens.device
+        if stream is None:
+            stream = torch.cuda.current_stream(dev)
+        q_start = torch.empty(kv.batch + 1, dtype=torch.int32, device=dev)
+        slot_map = torch.empty(max_slots, dtype=torch.int64, device=dev)
+        dkv_extend_tables(self.handle, kv.seq_lens_dev, new_lens, kv.batch, kv.table_dev, kv.stride, free_ids,
+                          free_ids.numel(), free_count, free_count, q_start, slot_map, max_slots, stream.cuda_stream)
+        return q_start, slot_map
+
+    def store(self, k_new, v_new, slot_map, kv: PagedKV, stream=None) -> None:
+        """Store k_new, v_new [rows, Hkv, D] (16-bit; rows may be strided, elements of a row are not) at slot_map."""
+        import torch
+        rows = k_new.shape[0]
+        for x in (k_new, v_new):
+            if x.shape != (rows, kv.num_kv_heads, kv.head_dim) or x.stride()[1:] != (kv.head_dim, 1):
+                raise ValueError("k_new and v_new are [rows, Hkv, D] with contiguous rows")
+        if k_new.stride(0) != v_new.stride(0):
+            raise ValueError("k_new and v_new have one row stride")
+        if slot_map.numel() < rows:
+            raise ValueError("slot_map holds fewer slots than there are rows")
+        if stream is None:
+            stream = torch.cuda.current_stream(k_new.device)
+        dkv_store_kv(self.handle, k_new, v_new, k_new.stride(0), slot_map, rows, kv.host_split, kv.k_host.ptr or None,
+                     kv.v_host.ptr or None, kv.k_dev if kv.num_dev_blocks else None,
+                     kv.v_dev if kv.num_dev_blocks else None, stream.cuda_stream, kv.num_dev_blocks)
+
+    def chunk(self, q, q_start, kv: PagedKV, out, window: int = 0, sinks: int = 0, include_self: bool = True,
+              k_stage=None, v_stage=None, stream=None) -> None:
+        """q, out [rows, Hq, D] (16-bit): rows q_start[b] .. q_start[b+1] are the new tokens of sequence b, at
+        positions seq_lens[b] ..; causal over the cache, under a window of tokens and sinks if window > 0."""
+        import torch
+        hq, d = self.cfg.num_q_heads, self.cfg.head_dim
+        if q.shape[1:] != (hq, d) or q.stride()[1:] != (d, 1) or out.shape != q.shape or not out.is_contiguous():
+            raise ValueError("q is [rows, Hq, D] with contiguous rows, out the same and contiguous")
+        if stream is None:
+            stream = torch.cuda.current_stream(q.device)
+        dkv_attn_chunk(self.handle, q, max(q.stride(0), hq * d), q_start, q.shape[0], kv.k_host.ptr or None,
+                       kv.v_host.ptr or None, kv.k_dev if kv.num_dev_blocks else None,
+                       kv.v_dev if kv.num_dev_blocks else None, kv.table_dev, kv.seq_lens_dev, kv.host_split, out,
+                       window, sinks, include_self, stream.cuda_stream, kv.batch, kv.stride, kv.num_dev_blocks,
+                       k_stage, v_stage)
+
+    def window(self, q, kv: PagedKV, out, window: int, sinks: int = 0, include_self: bool = False,
+               stream=None) -> None:
+        """q, out [B, Hq, D] fp32: decode attention over the last `window` tokens and the first `sinks`."""
+        import torch
+        if stream is None:
+            stream = torch.cuda.current_stream(q.device)
+        dkv_attn_decode_window(self.handle, window, sinks, include_self, q, kv.k_host.ptr or None,
+                               kv.v_host.ptr or None, kv.k_dev if kv.num_dev_blocks else None,
+                               kv.v_dev if kv.num_dev_blocks else None, kv.table_dev, kv.seq_lens_dev, kv.host_split,
+                               out, stream.cuda_stream, kv.batch, kv.stride, kv.num_dev_blocks)
 
     def status(self) -> int:
         return dkv_get_status(self.handle)

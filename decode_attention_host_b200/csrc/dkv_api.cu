@@ -12,6 +12,7 @@
 #include "dkv.h"
 #include "dkv_error.h"
 #include "dkv_append.cuh"
+#include "dkv_handle.h"
 #include "dkv_kernels.cuh"
 #include "dkv_multi.cuh"
 #include "dkv_plan.h"
@@ -34,28 +35,12 @@ int dkv::set_error(int code, const std::string& msg) { return fail(code, msg); }
 
 namespace {
 
-int cuda_fail(cudaError_t e, const char* what) {
-  g_err = std::string(what) + ": " + cudaGetErrorString(e);
-  return DKV_ERR_CUDA;
-}
-
-#define DKV_CUDA(call)                                  \
-  do {                                                  \
-    cudaError_t e_ = (call);                            \
-    if (e_ != cudaSuccess) return cuda_fail(e_, #call); \
-  } while (0)
-
-// Restores the caller's current device on scope exit.
-struct DeviceGuard {
-  int prev = -1;
-  bool ok = false;
-  explicit DeviceGuard(int dev) {
-    if (cudaGetDevice(&prev) == cudaSuccess) ok = cudaSetDevice(dev) == cudaSuccess;
-  }
-  ~DeviceGuard() {
-    if (prev >= 0) cudaSetDevice(prev);
-  }
-};
+using dkv::check_dev_pool;
+using dkv::check_host_pool;
+using dkv::cuda_fail;
+using dkv::DeviceGuard;
+using dkv::launch_merge;
+using dkv::SplitEntry;
 
 #ifndef DKV_HOST_STAGES
 #define DKV_HOST_STAGES 3
@@ -132,9 +117,6 @@ cudaError_t dev_alloc(void** p, size_t bytes, int* counter) {
 
 size_t split_smem(int D, int nst) { return dkv::split_smem_bytes(D, nst); }
 
-using SplitFn = void (*)(dim3, size_t, cudaStream_t, const dkv::SplitParams&, const dkv::TileMaps&);
-using SplitKernelPtr = const void*;
-
 template <int D, int G, bool BF16, int NST, bool ROPE, bool TMA>
 void launch_split(dim3 grid, size_t smem, cudaStream_t s, const dkv::SplitParams& p, const dkv::TileMaps& m) {
   dkv::split_kernel<D, G, BF16, NST, ROPE, TMA><<<grid, dkv::kThreads, smem, s>>>(p, m);
@@ -143,11 +125,6 @@ template <int D, int G, bool BF16, int NST, bool ROPE, bool TMA>
 const void* split_ptr() {
   return reinterpret_cast<const void*>(&dkv::split_kernel<D, G, BF16, NST, ROPE, TMA>);
 }
-
-struct SplitEntry {
-  SplitFn fn;
-  SplitKernelPtr ptr;
-};
 
 // TMA: the HBM launch (tiles by tensor copies); otherwise the zero-copy host
 // launch (16-byte cp.async from mapped host memory).
@@ -218,63 +195,7 @@ cudaError_t launch_append(bool bf16, int nb, dim3 grid, cudaStream_t s, const dk
   return bf16 ? launch_append_t<true>(nb, grid, s, ap) : launch_append_t<false>(nb, grid, s, ap);
 }
 
-// The merge, optionally as a programmatic dependent launch of the split kernel
-// just before it on the stream: its grid is set up while that kernel drains
-// and its first instruction waits for that kernel's results.
-using MergeFn = cudaError_t (*)(int, cudaStream_t, const dkv::MergeParams&, bool);
-template <int D>
-cudaError_t launch_merge(int rows, cudaStream_t s, const dkv::MergeParams& p, bool dependent) {
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(rows);
-  cfg.blockDim = dim3(32 * dkv::merge_warps(p.nslots, D));
-  cfg.dynamicSmemBytes = 0;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = dependent ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, dkv::merge_kernel<D>, p);
-}
-
 }  // namespace
-
-struct dkv_handle {
-  dkv_config cfg{};
-  int G = 0;
-  int sm_count = 0;
-  int beside_host = 0;        // HBM-kernel CTAs that fit on an SM beside a host-kernel CTA (0 or 1)
-  int units_target = 0;       // warps of the widest split launch (one resident wave: 2 CTAs per SM)
-  size_t part_rows = 0;
-  float qscale = 0.f;
-  int host_ctas = 0;           // the configuration's count; 0: chosen per call
-  float* part_o = nullptr;
-  float* part_lse = nullptr;
-  int32_t* status = nullptr;
-  int32_t* work = nullptr;    // [4]: work counters of the host-side and the device-side split launch
-  int2* lists = nullptr;      // [max_batch][max_blocks_per_seq]: per-pool block lists of a mixed call
-  int2* counts = nullptr;     // [max_batch]
-  double* inv_freq = nullptr;
-  cudaStream_t aux = nullptr;
-  cudaEvent_t ev_fork = nullptr;
-  cudaEvent_t ev_join = nullptr;
-  SplitEntry host_kernel{}, dev_kernel{}, dev_tma_kernel{}, multi_kernel{};  // dev: cp.async; dev_tma: tensor copies
-  // tensor maps of the last device pool and staging pool the HBM kernel read
-  struct PoolMaps {
-    const void* k = nullptr;
-    const void* v = nullptr;
-    long long rows = -1;
-    dkv::TileMaps maps{};
-  } dev_maps, stage_maps, host_maps;
-  MergeFn merge = nullptr;
-  const void* ok_host[2] = {nullptr, nullptr};
-  const void* ok_dev[4] = {nullptr, nullptr, nullptr, nullptr};
-  int last_launches = 0;
-  // per-kernel event pairs while profiling: [kernel][call] -> (start, stop)
-  int prof_capacity = 0;
-  int prof_used[3] = {0, 0, 0};
-  std::vector<cudaEvent_t> prof_events[3];
-};
 
 namespace {
 
@@ -377,34 +298,6 @@ int pool_maps(dkv_handle* h, dkv_handle::PoolMaps& cache, const void* k, const v
   return DKV_OK;
 }
 
-int check_host_pool(dkv_handle* h, const void* p, int which) {
-  if (h->ok_host[which] == p) return DKV_OK;
-  cudaPointerAttributes a{};
-  cudaError_t e = cudaPointerGetAttributes(&a, p);
-  if (e != cudaSuccess) {
-    cudaGetLastError();
-    return fail(DKV_ERR_INVALID_ARG, "host pool pointer is not known to CUDA (use dkv_host_pool_alloc)");
-  }
-  if (a.type != cudaMemoryTypeHost || a.devicePointer == nullptr || a.devicePointer != p)
-    return fail(DKV_ERR_INVALID_ARG, "host pool must be mapped pinned host memory passed by its device alias");
-  h->ok_host[which] = p;
-  return DKV_OK;
-}
-
-int check_dev_pool(dkv_handle* h, const void* p, int which) {
-  if (h->ok_dev[which] == p) return DKV_OK;
-  cudaPointerAttributes a{};
-  cudaError_t e = cudaPointerGetAttributes(&a, p);
-  if (e != cudaSuccess) {
-    cudaGetLastError();
-    return fail(DKV_ERR_INVALID_ARG, "device pool pointer is not known to CUDA");
-  }
-  if (!((a.type == cudaMemoryTypeDevice || a.type == cudaMemoryTypeManaged) && a.device == h->cfg.device))
-    return fail(DKV_ERR_INVALID_ARG, "device pool must be device memory of the handle's GPU");
-  h->ok_dev[which] = p;
-  return DKV_OK;
-}
-
 }  // namespace
 
 extern "C" {
@@ -479,6 +372,8 @@ int dkv_create(const dkv_config* cfg, dkv_handle** out) {
   e = cudaFuncSetAttribute(h->multi_kernel.ptr, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            static_cast<int>(multi_smem(c.head_dim)));
   if (e != cudaSuccess) return bail(cuda_fail(e, "cudaFuncSetAttribute(multi-token kernel)"));
+  e = dkv::prepare_serving(h);
+  if (e != cudaSuccess) return bail(cuda_fail(e, "cudaFuncSetAttribute(serving kernels)"));
   // every kernel of a step prefers the largest shared-memory carveout, so an SM
   // need not change its L1/shared split between the step's kernels
   {
@@ -496,10 +391,10 @@ int dkv_create(const dkv_config* cfg, dkv_handle** out) {
   if (dev_alloc(reinterpret_cast<void**>(&h->part_o), h->part_rows * c.head_dim * sizeof(float), &nalloc) ||
       dev_alloc(reinterpret_cast<void**>(&h->part_lse), h->part_rows * sizeof(float), &nalloc) ||
       dev_alloc(reinterpret_cast<void**>(&h->status), sizeof(int32_t), &nalloc) ||
-      dev_alloc(reinterpret_cast<void**>(&h->work), 4 * sizeof(int32_t), &nalloc) ||
+      dev_alloc(reinterpret_cast<void**>(&h->work), dkv::kWorkWords * sizeof(int32_t), &nalloc) ||
       dev_alloc(reinterpret_cast<void**>(&h->lists), list_entries * sizeof(int2), &nalloc) ||
       dev_alloc(reinterpret_cast<void**>(&h->counts), c.max_batch * sizeof(int2), &nalloc) ||
-      dev_alloc(reinterpret_cast<void**>(&h->inv_freq), sizeof(double) * (c.head_dim / 2), &nalloc)) {
+      dev_alloc(reinterpret_cast<void**>(&h->inv_freq), 2 * sizeof(double) * (c.head_dim / 2), &nalloc)) {
     cudaGetLastError();
     return bail(fail(DKV_ERR_NO_MEMORY, "workspace allocation failed"));
   }
@@ -508,9 +403,13 @@ int dkv_create(const dkv_config* cfg, dkv_handle** out) {
   dkv::rope_frequencies(c.rope_base, c.head_dim, freq);
   e = cudaMemcpy(h->inv_freq, freq, sizeof(double) * (c.head_dim / 2), cudaMemcpyHostToDevice);
   if (e != cudaSuccess) return bail(cuda_fail(e, "cudaMemcpy(inv_freq)"));
+  uint64_t turns[64];
+  dkv::rope_turns(freq, c.head_dim, turns);
+  e = cudaMemcpy(h->inv_freq + c.head_dim / 2, turns, sizeof(uint64_t) * (c.head_dim / 2), cudaMemcpyHostToDevice);
+  if (e != cudaSuccess) return bail(cuda_fail(e, "cudaMemcpy(rope turns)"));
   e = cudaMemset(h->status, 0, sizeof(int32_t));
   if (e != cudaSuccess) return bail(cuda_fail(e, "cudaMemset(status)"));
-  e = cudaMemset(h->work, 0, 4 * sizeof(int32_t));
+  e = cudaMemset(h->work, 0, dkv::kWorkWords * sizeof(int32_t));
   if (e != cudaSuccess) return bail(cuda_fail(e, "cudaMemset(work counters)"));
   int lo = 0, hi = 0;
   e = cudaDeviceGetStreamPriorityRange(&lo, &hi);

@@ -105,6 +105,11 @@ struct SplitParams {
   int32_t stall_first_copy; // test hook: the first tile of unit 0 arms its barrier but issues no copy
   int32_t extra_tokens;     // tokens past seq_lens that belong to the unit (multi-token queries: Tq - 1)
   int32_t num_queries;      // query tokens per sequence (1 for decode)
+  // windowed launches (split_kernel<..., WIN>): one launch walks the visible blocks of both pools
+  const uint16_t* k_host;   // the mapped host pools; ids in [0, host_split) live there, k_pool / v_pool hold the rest
+  const uint16_t* v_host;
+  int32_t host_split;
+  int32_t window, sinks;    // visible: the last `window` tokens, and the first `sinks`
   InvDiv div_hkv, div_nsplit, div_bs;  // hkv, nsplit, block_size (set_divisors)
 };
 
@@ -455,9 +460,19 @@ __device__ __forceinline__ void split_hi_lo(float2 p, uint32_t& hi, uint32_t& lo
 // [c*n', (c+1)*n') of the sequence's list of this pool's blocks, n' =
 // max(bps, ceil(n/nsplit)), so every split of a launch holds blocks of its
 // own pool and the work of a launch is even whatever the placement.
-struct TileStream {
+//
+// WIN: the visible tokens of a sequence are the first `sinks` and the last
+// `window` of its L.  Its virtual block list is the blocks that hold sinks,
+// then those that hold the window (a block that holds both counts once);
+// split c covers entries [c*n', (c+1)*n') of it, so table entries of blocks
+// without a visible token are never read.  One launch serves both pools: a
+// host block's tile carries ~id as its index.  `gap` describes the tile just
+// returned: its rows in [gap & 31, gap >> 5) are not visible.
+template <bool WIN>
+struct TileStreamT {
   int unit;
   int b, h, L, j, j_end, sub, pidx, blk;
+  int lo, sk, nsb, wb0, gap;   // WIN: window start, visible sinks before it, sink blocks, first window block
   const int2* lbase;
   bool started, emitted, bad_len;
 
@@ -474,9 +489,19 @@ struct TileStream {
     b = p.div_nsplit.div(bc);
     const int c = bc - b * p.nsplit;
     L = p.seq_lens[b];
-    bad_len = (L < 0 || L + p.extra_tokens > p.max_len);
+    bad_len = (L < 0 || L > p.max_len - p.extra_tokens);
     L += p.extra_tokens;
-    if (p.lists) {
+    if constexpr (WIN) {
+      const int Lv = bad_len ? 0 : L;
+      lo = max(0, Lv - p.window);
+      sk = min(p.sinks, lo);
+      wb0 = p.div_bs.div(lo);
+      nsb = min(p.div_bs.div(sk + p.block_size - 1), wb0);
+      const int n = p.div_bs.div(Lv + p.block_size - 1) - wb0 + nsb;
+      const int per = max(p.bps, p.div_nsplit.div(n + p.nsplit - 1));
+      j = min(c * per, n);
+      j_end = min(j + per, n);
+    } else if (p.lists) {
       const int2 cnt = p.counts[b];
       const int n = bad_len ? 0 : (p.list_dev ? cnt.y : cnt.x);
       lbase = p.lists + static_cast<size_t>(b) * p.list_stride + (p.list_dev ? p.list_stride - n : 0);
@@ -505,7 +530,10 @@ struct TileStream {
       while (j < j_end) {
         if (sub == 0) {
           int id;
-          if (p.lists) {
+          if constexpr (WIN) {
+            blk = j < nsb ? j : wb0 + j - nsb;
+            id = p.table[static_cast<size_t>(b) * p.stride + blk];
+          } else if (p.lists) {
             const int2 e = lbase[j];
             blk = e.x;
             id = e.y;
@@ -513,9 +541,11 @@ struct TileStream {
             blk = j;
             id = p.table[static_cast<size_t>(b) * p.stride + j];
           }
-          if (id >= p.id_lo && id < p.id_hi) {
+          if (WIN && id >= 0 && id < p.id_total) {
+            pidx = id < p.host_split ? ~id : id - p.host_split;
+          } else if (!WIN && id >= p.id_lo && id < p.id_hi) {
             pidx = id - p.id_lo;
-          } else if (id >= 0 && id < p.id_total) {
+          } else if (!WIN && id >= 0 && id < p.id_total) {
             ++j;  // lives in the other pool
             continue;
           } else {
@@ -528,12 +558,19 @@ struct TileStream {
         const int p0 = blk * p.block_size + sub * kTileTokens;
         const int nvalid = min(kTileTokens, L - p0);
         TileDesc d{unit, pidx, p0, nvalid | (sub << kSubShift) | (h << 16)};
-        emitted = true;
+        if constexpr (WIN) {
+          // rows [max(sk - p0, 0), lo - p0) of the tile lie between the sinks and the window
+          const int g0 = min(max(sk - p0, 0), kTileTokens), g1 = min(max(lo - p0, 0), kTileTokens);
+          gap = g0 < g1 ? g0 | (g1 << 5) : 0;
+        }
+        const bool skip = WIN && gap == (kTileTokens << 5);   // no visible row
+        if (!skip) emitted = true;
         ++sub;
         if (sub * kTileTokens >= p.block_size || p0 + kTileTokens >= L) {
           sub = 0;
           ++j;
         }
+        if (skip) continue;
         return d;
       }
       const bool was_emitted = emitted;
@@ -544,6 +581,8 @@ struct TileStream {
     return TileDesc{-1, 0, 0, 0};
   }
 };
+
+using TileStream = TileStreamT<false>;
 
 // End of a split launch: lets a dependent launch (the merge) be scheduled,
 // then the last CTA to finish clears the work counter for the next launch on
@@ -652,10 +691,11 @@ __host__ __device__ constexpr size_t split_smem_bytes(int D, int nst) {
          (D == 64 ? sizeof(SplitSmemTail<4, 4>) : sizeof(SplitSmemTail<8, 4>));
 }
 
-template <int D, int G, bool BF16, int NST, bool ROPE, bool TMA>
+template <int D, int G, bool BF16, int NST, bool ROPE, bool TMA, bool WIN = false>
 __global__ void __launch_bounds__(kThreads) split_kernel(const SplitParams p, const __grid_constant__ TileMaps maps) {
   static_assert(G >= 1 && G <= 4, "query group of 1, 2 or 4 heads");
   static_assert(NST <= 4, "SplitSmemTail is sized for up to 4 stages");
+  static_assert(!(WIN && TMA), "windowed launches read both pools with cp.async");
   constexpr int PPL = D / 16;                  // NeoX pairs per lane
   constexpr int NP2 = PPL / 2;                 // fp32 pairs per half-row per lane
   constexpr int ROW = D * 2;                   // bytes of one token row
@@ -704,8 +744,9 @@ __global__ void __launch_bounds__(kThreads) split_kernel(const SplitParams p, co
     rf[j] = s_rope.f[j][li];
   }
 
-  TileStream ts;
+  TileStreamT<WIN> ts;
   ts.grab(p, lane);
+  __shared__ int s_gap[WIN ? kWarps : 1][NST];   // WIN: the invisible rows of each stage's tile
 
   // Tile copies.  TMA: lane 0 arms the stage's barrier with the tile's bytes
   // and issues D/64 boxes for K and for V; a stage with nothing to copy gets a
@@ -733,6 +774,9 @@ __global__ void __launch_bounds__(kThreads) split_kernel(const SplitParams p, co
   uint32_t inflight = 0;  // per stage: tensor copies issued and not yet waited for (TMA)
   bool broken = false;    // a copy did not complete in time: no more copies, every later tile poisoned (TMA)
   auto issue = [&](const TileDesc& d, int slot) {
+    if constexpr (WIN) {
+      if (lane == 0) s_gap[warp][slot] = ts.gap;
+    }
     const int nvalid = d.meta & 0xff;
     const bool copy = !(d.unit < 0 || (d.meta & kFlagPoison) || nvalid == 0);
     const int h = d.meta >> 16;
@@ -763,10 +807,12 @@ __global__ void __launch_bounds__(kThreads) split_kernel(const SplitParams p, co
       }
     } else {
       if (!copy) return;
-      const size_t row0 = (static_cast<size_t>(d.pidx) * p.hkv + h) * p.block_size + sub * kTileTokens;
-      const char* gk = reinterpret_cast<const char*>(p.k_pool + row0 * D) + lane * 16;
-      const char* gv = reinterpret_cast<const char*>(p.v_pool + row0 * D) + lane * 16;
-      if (nvalid == kTileTokens) {
+      const bool on_host = WIN && d.pidx < 0;
+      const int pidx = on_host ? ~d.pidx : d.pidx;
+      const size_t row0 = (static_cast<size_t>(pidx) * p.hkv + h) * p.block_size + sub * kTileTokens;
+      const char* gk = reinterpret_cast<const char*>((on_host ? p.k_host : p.k_pool) + row0 * D) + lane * 16;
+      const char* gv = reinterpret_cast<const char*>((on_host ? p.v_host : p.v_pool) + row0 * D) + lane * 16;
+      if (nvalid == kTileTokens && !(WIN && ts.gap)) {
 #pragma unroll
         for (int k = 0; k < KCOPIES; ++k) {
           cp_async16(sk + lane * 16 + 512 * k, gk + 512 * k, 16);
@@ -775,7 +821,9 @@ __global__ void __launch_bounds__(kThreads) split_kernel(const SplitParams p, co
       } else {
 #pragma unroll
         for (int k = 0; k < KCOPIES; ++k) {
-          const int nb = (lane + 32 * k) / CPR < nvalid ? 16 : 0;   // rows past the end: zeros, nothing read
+          const int r = (lane + 32 * k) / CPR;
+          // rows past the end or out of sight: zeros, nothing read
+          const int nb = r < nvalid && !(WIN && r >= (ts.gap & 31) && r < (ts.gap >> 5)) ? 16 : 0;
           cp_async16(sk + lane * 16 + 512 * k, nb ? gk + 512 * k : gk - lane * 16, nb);
           cp_async16(sv + dofs[k & 3] + (k >> 2) * 1024, nb ? gv + 512 * k : gv - lane * 16, nb);
         }
@@ -832,6 +880,9 @@ __global__ void __launch_bounds__(kThreads) split_kernel(const SplitParams p, co
   int next_pos = -1, chain = 0;
 
   auto init_unit = [&](int unit, int h) {
+    // a fresh seed for every unit: which units a warp takes one after another
+    // then has no effect on the result, bit for bit
+    if constexpr (WIN) next_pos = -1;
     const int b = p.div_nsplit.div(p.div_hkv.div(unit));
     const int L = p.seq_lens[b];
     float2 C[NP2], S[NP2];
@@ -908,6 +959,7 @@ __global__ void __launch_bounds__(kThreads) split_kernel(const SplitParams p, co
     const char* sk = ring + static_cast<size_t>(slot) * 2 * TILE;
     const char* sv = sk + TILE;
     const int nvalid = d.meta & 0xff;
+    const int gap = WIN ? s_gap[warp][slot] : 0;
     // ---- scores: rotate K rows on the fly (CUDA cores, fp32 pairs).  The
     // rotation state (Cc, Sc) carries over when this tile continues the
     // previous one; a fresh fp64-reduced seed at least every 16 tiles.
@@ -961,7 +1013,8 @@ __global__ void __launch_bounds__(kThreads) split_kernel(const SplitParams p, co
     for (int k = 0; k < NH; ++k) {
       const int j = (G == 4) ? (li * 2 + k) : (G == 2 ? li : (li >> 1));
       mt[k] = j & 3;
-      sc[k] = (tg + 4 * mt[k]) < nvalid ? v[k] : -INFINITY;
+      const int r = tg + 4 * mt[k];
+      sc[k] = r < nvalid && !(WIN && r >= (gap & 31) && r < (gap >> 5)) ? v[k] : -INFINITY;
     }
     // ---- online softmax for head gl.  The reference max mrun (shared by the
     // head's lanes) is raised only when a score of the tile exceeds it by more

@@ -72,6 +72,16 @@ inline void rope_frequencies(double base, int D, double* freq) {
   for (int i = 0; i < D / 2; ++i) freq[i] = base > 0.0 ? std::pow(base, -2.0 * i / static_cast<double>(D)) : 0.0;
 }
 
+// The same frequencies as a fraction of a turn per position, in units of 2^-64
+// turns: p * turns[i] mod 2^64 is then the angle of position p modulo one turn,
+// off by at most (p + 1) * 2^-64 turns plus the rounding of freq itself
+// (2^-53 relative), with one integer product and no range reduction.
+inline void rope_turns(const double* freq, int D, uint64_t* turns) {
+  for (int i = 0; i < D / 2; ++i)
+    turns[i] = static_cast<uint64_t>(static_cast<long double>(freq[i]) / 6.283185307179586476925286766559L *
+                                         18446744073709551616.0L + 0.5L);
+}
+
 // ---- scratch layout of the allocation-free entry point -----------------------
 // [0, 256): status word and the two launches' work counters; [256, 1024): the
 // RoPE frequencies; then the per-sequence pool counts, the pool lists, the

@@ -56,6 +56,8 @@ extern "C" {
 #define DKV_STATUS_COPY_TIMEOUT 4 /* a tile copy into shared memory did not complete within 2 s; the
                                      affected rows are NaN (the kernel stopped copying and returned) */
 #define DKV_STATUS_INTERNAL 8     /* the HBM kernel found its shared memory misaligned and did nothing */
+#define DKV_STATUS_NO_FREE_BLOCKS 16 /* dkv_extend_tables: the free list holds too few blocks (nothing was changed) */
+#define DKV_STATUS_NO_SLOTS 32    /* dkv_extend_tables: more new tokens than max_slots (nothing was changed) */
 
 typedef enum { DKV_KV_F16 = 0, DKV_KV_BF16 = 1 } dkv_kv_dtype;
 
@@ -195,6 +197,120 @@ DKV_API int dkv_append_kv(dkv_handle* h, const float* x, const void* w_k, const 
                           const int32_t* block_table, const int32_t* seq_lens, int32_t host_split, void* k_host,
                           void* v_host, void* k_dev, void* v_dev, dkv_stream_t stream, int32_t batch,
                           int32_t block_table_stride, int32_t num_dev_blocks);
+
+/* ---- a serving step around the cache ---------------------------------------
+ * The calls an engine makes, in order, on a cache that grows: give the new
+ * tokens of every request blocks and slots, store their K/V, run attention
+ * (chunks of new tokens, or one token per sequence under a sliding window).
+ * All of them take device pointers, run on `stream`, neither allocate nor
+ * synchronise, and may be captured into a CUDA graph; lengths, tables and the
+ * free list are read on the device, so a captured step follows them.  Like
+ * dkv_attn_decode they use the handle's workspace: one call at a time per
+ * handle.  Block ids and pools are those of dkv_attn_decode. */
+
+/*
+ * dkv_extend_tables -- grow the block tables by this step's new tokens and
+ * map each of them to its slot.  Sequence b holds seq_lens[b] tokens in the
+ * first ceil(seq_lens[b]/S) entries of its table row and gets new_lens[b]
+ * more (0 is allowed); the blocks it lacks are taken from the top of a stack of free ids,
+ * in order of sequence, then of position.
+ *   seq_lens, new_lens  device int32 [batch], both >= 0, their sum at most
+ *                 min(block_table_stride, max_blocks_per_seq) * S
+ *   block_table   device int32 [batch][block_table_stride]: entries of new
+ *                 blocks are written, all others left as they are
+ *   free_ids      device int32 [free_capacity]; free_count device int32 [1]:
+ *                 the stack's entries are free_ids[0 .. free_count), the k-th
+ *                 block taken is free_ids[free_count - 1 - k]
+ *   free_left     device int32 [1], written: free_count less the blocks taken;
+ *                 may be free_count itself
+ *   q_start       device int32 [batch + 1], written: q_start[b] new tokens
+ *                 precede those of sequence b (the row offsets dkv_attn_chunk takes)
+ *   slot_map      device int64 [max_slots], 8-byte aligned, written: entry
+ *                 q_start[b] + i is the slot id * S + row of token
+ *                 seq_lens[b] + i of sequence b (the slots dkv_store_kv takes);
+ *                 entries behind the last token are -1.  max_slots <= 2^30.
+ * seq_lens is not changed; the caller advances it.  All or nothing: with a
+ * length out of range (DKV_STATUS_BAD_SEQ_LEN), too few free blocks
+ * (DKV_STATUS_NO_FREE_BLOCKS) or more new tokens than max_slots
+ * (DKV_STATUS_NO_SLOTS) the table and the free list stay as they are, q_start
+ * is all 0 and slot_map all -1, so that the step's other calls do nothing.  A
+ * negative id met in a table or on the stack maps its tokens to -1 and sets
+ * DKV_STATUS_BAD_BLOCK_ID.  1 <= batch <= min(max_batch, 8192).
+ * Errors: INVALID_ARG, UNSUPPORTED (batch above 8192), CUDA. */
+DKV_API int dkv_extend_tables(dkv_handle* h, const int32_t* seq_lens, const int32_t* new_lens, int32_t batch,
+                              int32_t* block_table, int32_t block_table_stride, const int32_t* free_ids,
+                              int32_t free_capacity, const int32_t* free_count, int32_t* free_left, int32_t* q_start,
+                              int64_t* slot_map, int32_t max_slots, dkv_stream_t stream);
+
+/*
+ * dkv_store_kv -- store K/V rows (un-rotated) at their slots.
+ *   k_new, v_new  device, 16-bit (the handle's kv_dtype): row i holds Hkv * D
+ *                 elements, head after head, and starts row_stride elements
+ *                 after row i - 1 (row_stride >= Hkv * D, a multiple of 8, so
+ *                 that both may be slices of a fused projection's rows);
+ *                 16-byte aligned
+ *   slot_map      device int64 [num_rows]: block id * S + row in the block; a
+ *                 negative slot skips its row
+ * Host-resident blocks are written through the mapped pointer.  A slot of an
+ * id outside both pools sets DKV_STATUS_BAD_BLOCK_ID and is skipped.  The
+ * slots of a call must differ: of two rows with the same slot it is not
+ * specified which one's values stay.  Errors: INVALID_ARG, CUDA. */
+DKV_API int dkv_store_kv(dkv_handle* h, const void* k_new, const void* v_new, int64_t row_stride,
+                         const int64_t* slot_map, int32_t num_rows, int32_t host_split, void* k_host, void* v_host,
+                         void* k_dev, void* v_dev, dkv_stream_t stream, int32_t num_dev_blocks);
+
+/*
+ * dkv_attn_chunk -- attention of a chunk of new tokens per sequence over the
+ * paged cache (prefill, chunked prefill, verification of drafts), ragged
+ * batches packed row after row.  Query i of sequence b is row q_start[b] + i,
+ * sits at position L_b + i (L_b = seq_lens[b]: the tokens cached before the
+ * chunk) and, with hi = L_b + i + include_self, sees the cached tokens
+ *     t < hi                                     when window == 0,
+ *     t < hi with t >= hi - window or t < sinks  when window > 0.
+ * include_self = 1 is the usual causal mask (the chunk's own K/V are in the
+ * cache, see dkv_store_kv); 0 is the mask of dkv_attn_decode_multi.  A row
+ * that sees no token is zero.
+ *   q, out        device, 16-bit (the handle's kv_dtype), q un-rotated: row r
+ *                 of q starts q_stride elements after row r - 1 (q_stride >=
+ *                 Hq * D, a multiple of 8); out is [total_rows][Hq][D]; both
+ *                 16-byte aligned
+ *   q_start       device int32 [batch + 1], not decreasing, q_start[0] = 0;
+ *                 sequences may have no row.  Rows from q_start[batch] on are
+ *                 left as they were; q_start[batch] <= total_rows.
+ *   seq_lens      L_b >= 0; L_b + (rows of b) at most
+ *                 min(block_table_stride, max_blocks_per_seq) * S, else
+ *                 DKV_STATUS_BAD_SEQ_LEN and NaN rows.  Table entries of
+ *                 blocks that no row of a sequence sees are not read.
+ *   k_stage, v_stage  NULL, or device memory (HBM) of >= host_split blocks
+ *                 each, pool layout, 16-byte aligned.  Without them
+ *                 host-resident blocks are read in place over PCIe, once for
+ *                 every 256 / (Hq/Hkv) rows of a chunk; with them the first
+ *                 host_split blocks of the host pools are copied there first.
+ * Scores, softmax statistics and outputs are accumulated in fp32.  The stored
+ * V rows of tokens that some row of the sequence sees must be finite.
+ * Errors: INVALID_ARG, CUDA. */
+DKV_API int dkv_attn_chunk(dkv_handle* h, const void* q, int64_t q_stride, const int32_t* q_start,
+                           int32_t total_rows, const void* k_host, const void* v_host, const void* k_dev,
+                           const void* v_dev, const int32_t* block_table, const int32_t* seq_lens,
+                           int32_t host_split, void* out, int32_t window, int32_t sinks, int32_t include_self,
+                           dkv_stream_t stream, int32_t batch, int32_t block_table_stride, int32_t num_dev_blocks,
+                           void* k_stage, void* v_stage);
+
+/*
+ * dkv_attn_decode_window -- dkv_attn_decode under a sliding window with sinks:
+ * with hi = L_b + include_self the query (at position L_b) sees the last
+ * `window` (>= 1) tokens t in [hi - window, hi) and the first `sinks` (>= 0)
+ * tokens.  include_self = 1 counts token L_b itself, whose K/V the cache must
+ * then hold (see dkv_append_kv, dkv_store_kv).  Table entries of blocks
+ * without a visible token are not read, so evicted blocks may be given away.
+ * One launch reads the blocks of both pools, host-resident ones (sinks, say)
+ * zero-copy.  The other arguments, the layouts and the errors are those of
+ * dkv_attn_decode; L_b + include_self is limited as L_b is there. */
+DKV_API int dkv_attn_decode_window(dkv_handle* h, int32_t window, int32_t sinks, int32_t include_self, const float* q,
+                                   const void* k_host, const void* v_host, const void* k_dev, const void* v_dev,
+                                   const int32_t* block_table, const int32_t* seq_lens, int32_t host_split,
+                                   float* out, dkv_stream_t stream, int32_t batch, int32_t block_table_stride,
+                                   int32_t num_dev_blocks);
 
 /* dkv_get_status -- synchronise the handle's device, return the accumulated
  * DKV_STATUS_* bits in *status and clear them. */
