@@ -35,6 +35,7 @@ DKV_STATUS_COPY_TIMEOUT = 4
 DKV_STATUS_INTERNAL = 8
 DKV_STATUS_NO_FREE_BLOCKS = 16
 DKV_STATUS_NO_SLOTS = 32
+DKV_STATUS_RANGE = 64
 DKV_KV_F16 = 0
 DKV_KV_BF16 = 1
 DKV_PLACE_PREFIX_HOST = 0

@@ -1,34 +1,180 @@
 // dkv_chunk.cuh -- attention of a chunk of new tokens per sequence over the
-// paged cache.
+// paged cache, on the 5th-generation tensor cores.
 //
 // Query i of sequence b sits at position L_b + i.  With hi = L_b + i + self it
 // sees the cached tokens t < hi, and under a window only those with
 // t >= hi - window or t < sinks:
 //     s_t = scale * (R(L_b + i) q) . (R(t) k_t),   o = sum_t softmax(s)_t v_t.
 // A row that sees nothing is zero.
+//
+// Work.  The G query heads of a kv head share its K and V, so the rows of a
+// (sequence, kv head) are its tokens times G, token-major, and a CTA takes 256
+// of them as two tiles of 128 (the M of one tcgen05.mma).  It walks the 128-
+// token tiles that some row of it sees: the tiles that hold sinks, then those
+// from the first row's window start to the last row's end.  With few row tiles
+// the walk is cut into splits whose partial results a second kernel joins.
+//
+// One CTA per SM, 16 warps:
+//   warp 0      copies K and V tiles, one tensor copy per run of rows that lies
+//               in one block (16 to 128 rows) and 64-element half
+//   warp 1      issues the matrix instructions: S = Q K^T into TMEM, then
+//               O += P V with P read from TMEM; the two row tiles alternate, so
+//               one's softmax runs under the other's products
+//   warps 4-7   rotate each K tile in place: keys are cached un-rotated, and a
+//               tile that is rotated once serves 256 rows
+//   warps 8-11, 12-15  the softmax of row tile 0 and 1, a thread per row: no
+//               value leaves its thread, the running maximum is raised lazily
+//               (only past 2^8, so O is rescaled rarely), P goes back to TMEM
+//               over the S it came from
+//
+// Roundings to 16 bits: rotated queries and keys are held in fp16 for both
+// cache types (fp32 rotation, one rounding to 2^-11; bf16 operands would be
+// off by 2^-8, the largest error of the whole computation), unrotated ones as
+// stored; the weights P take V's type, as one instruction multiplies equal
+// types.  Everything else is fp32.  A rotated component beyond fp16's range
+// poisons the rows that see it and sets a status bit.
 #pragma once
 
 #include "dkv_kernels.cuh"
 
 namespace dkv {
 
+constexpr int kChunkTokens = 128;                  // tokens of a K/V tile, the N of S = Q K^T
+constexpr int kChunkRows = 256;                    // rows of a CTA: two tiles of 128
+constexpr int kChunkThreads = 512;
+constexpr int kSubTile = kChunkTokens * 128;       // bytes of 128 rows x 64 elements, 128-byte swizzle
+constexpr int kRopeChain = 8;                      // K tiles that may follow one seed of the rotation
+// Registers per thread of the four warp groups, out of the 128 per thread the
+// block is launched with: the shares add up to exactly those.
+constexpr int kRegsLaunch = 128;
+constexpr int kRegsIssue = 48;
+constexpr int kRegsRotate = 96;
+constexpr int kRegsSoftmax = 184;
+static_assert(kRegsIssue + kRegsRotate + 2 * kRegsSoftmax <= 4 * kRegsLaunch, "setmaxnreg.inc would wait for ever");
+constexpr int kStatusRange = 64;                   // DKV_STATUS_RANGE
+
 struct ChunkParams {
   const uint16_t* q;          // [total_rows] of hq * D elements, q_stride elements apart
   uint16_t* out;              // [total_rows][hq][D]
-  const uint16_t* k_host;     // block ids [0, host_split)
-  const uint16_t* v_host;
-  const uint16_t* k_dev;      // block ids [host_split, id_total)
-  const uint16_t* v_dev;
   const int32_t* q_start;     // [batch + 1]
   const int32_t* seq_lens;    // [batch]
   const int32_t* table;       // [batch][stride]
   const uint64_t* turns;      // [D / 2] turns per position, 2^-64 turns
+  float* part_o;              // [total_rows][hq][nsplit][D], nsplit > 1
+  float* part_lse;            // [total_rows][hq][nsplit], log2 domain
   int32_t* status;
   long long q_stride;
   int32_t total_rows, batch, stride, hq, hkv, block_size, host_split, id_total, max_len;
+  int32_t group_shift;        // log2(hq / hkv)
+  int32_t nsplit;
+  int32_t box;                // rows of one tensor copy: the largest power of two that divides the block, up to 128
+  int32_t oob_row;            // a row outside the pool of `oob_host`: copies from there fill with zeros
+  int32_t oob_host;
   int32_t window, sinks, self;
   float qscale;               // softmax scale * log2(e)
+  InvDiv div_bs, div_hkv, div_split;
 };
+
+// Tensor maps of the four pools: boxes of `box` rows x 64 elements, 128-byte swizzle.
+struct ChunkMaps {
+  CUtensorMap k_dev, v_dev, k_host, v_host;
+};
+
+template <int D>
+struct ChunkShape {
+  static constexpr int kSub = D / 64;                       // 64-element halves of a row
+  static constexpr int kTile = kSub * kSubTile;             // bytes of a Q, K or V tile
+  static constexpr int kStagesK = D == 128 ? 3 : 4;
+  static constexpr int kStagesV = D == 128 ? 2 : 4;
+};
+
+struct ChunkTail {
+  uint64_t k_full[4], k_ready[4], k_free[4];   // copied, rotated, read by the products of both row tiles
+  uint64_t v_full[4], v_free[4];
+  uint64_t q_ready[2], s_full[2], p_ready[2];  // per row tile
+  uint64_t done;                               // every product has completed
+  uint32_t tmem;
+  int32_t b, tile;                             // the CTA's sequence (-1: none) and row tile
+  int32_t poison;                              // an invalid block id or an operand out of range
+  int32_t broken;                              // a wait ran out: every role gives up
+};
+
+template <int D>
+__host__ __device__ constexpr size_t chunk_smem_bytes() {
+  using C = ChunkShape<D>;
+  return static_cast<size_t>(2 + C::kStagesK + C::kStagesV) * C::kTile + sizeof(ChunkTail);
+}
+
+// ----------------------------------------------------------------------------- tensor core helpers
+
+// Shared-memory matrix descriptor, 128-byte swizzle: start address, the two
+// strides in 16-byte units, descriptor version 1, swizzle mode 2.
+__device__ __forceinline__ uint64_t umma_desc(uint32_t addr, uint32_t lead, uint32_t stride) {
+  return static_cast<uint64_t>((addr >> 4) & 0x3fff) | (static_cast<uint64_t>(lead >> 4) << 16) |
+         (static_cast<uint64_t>(stride >> 4) << 32) | (1ull << 46) | (2ull << 61);
+}
+
+// Instruction descriptor of kind::f16: fp32 accumulator, A and B both fp16 or
+// both bf16, A K-major, B K-major or (mn) N-major.
+__host__ __device__ constexpr uint32_t umma_idesc(int m, int n, bool bf16, bool mn) {
+  return (1u << 4) | (bf16 ? (1u << 7) | (1u << 10) : 0u) | (mn ? 1u << 16 : 0u) |
+         (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(m >> 4) << 24);
+}
+
+__device__ __forceinline__ void umma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc),
+      "r"(static_cast<uint32_t>(acc))
+      : "memory");
+}
+__device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(idesc),
+      "r"(static_cast<uint32_t>(acc))
+      : "memory");
+}
+// One arrival on `bar` when all matrix instructions this thread has issued are complete.
+__device__ __forceinline__ void umma_commit(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void tmem_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tmem_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+
+#define DKV_R8(r, i) "+r"(r[i]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3]), "+r"(r[i + 4]), "+r"(r[i + 5]), \
+                     "+r"(r[i + 6]), "+r"(r[i + 7])
+#define DKV_O8(r, i) "=r"(r[i]), "=r"(r[i + 1]), "=r"(r[i + 2]), "=r"(r[i + 3]), "=r"(r[i + 4]), "=r"(r[i + 5]), \
+                     "=r"(r[i + 6]), "=r"(r[i + 7])
+#define DKV_I8(r, i) "r"(r[i]), "r"(r[i + 1]), "r"(r[i + 2]), "r"(r[i + 3]), "r"(r[i + 4]), "r"(r[i + 5]), \
+                     "r"(r[i + 6]), "r"(r[i + 7])
+
+// 32 columns of this warp's 32 TMEM lanes, one lane per thread.
+__device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
+      "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : DKV_O8(r, 0), DKV_O8(r, 8), DKV_O8(r, 16), DKV_O8(r, 24)
+      : "r"(addr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,"
+      "%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::DKV_I8(r, 0), DKV_I8(r, 8), DKV_I8(r, 16),
+      DKV_I8(r, 24), "r"(addr)
+      : "memory");
+}
+// Completes this thread's loads; the registers pass through, so no use of them moves above it.
+__device__ __forceinline__ void tmem_ld_wait(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" : DKV_R8(r, 0), DKV_R8(r, 8), DKV_R8(r, 16), DKV_R8(r, 24)::"memory");
+}
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+#undef DKV_R8
+#undef DKV_O8
+#undef DKV_I8
+
+// ----------------------------------------------------------------------------- small helpers
 
 // cos / sin of position pos for a pair of `turns` per position: the product
 // modulo 2^64 is the angle modulo one turn, its top 32 bits as a signed number
@@ -39,107 +185,597 @@ __device__ __forceinline__ void turn_cs(int pos, uint64_t turns, float& c, float
 }
 
 template <bool BF16>
-__device__ __forceinline__ float widen1(uint16_t x) {
-  return BF16 ? __uint_as_float(static_cast<uint32_t>(x) << 16) : __half2float(__ushort_as_half(x));
-}
-template <bool BF16>
-__device__ __forceinline__ uint16_t narrow1(float x) {
-  return BF16 ? __bfloat16_as_ushort(__float2bfloat16_rn(x)) : __half_as_ushort(__float2half_rn(x));
+__device__ __forceinline__ uint32_t narrow2(float x, float y) {
+  if constexpr (BF16) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  } else {
+    const __half2 h = __floats2half2_rn(x, y);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
 }
 
-// One warp per (row, kv head): lane l holds the pairs l, l + 32 of the G
-// queries and walks the visible tokens one by one with an online softmax.
-template <int D, int G, bool BF16, bool ROPE>
-__global__ void __launch_bounds__(128) chunk_row_kernel(const ChunkParams p) {
-  constexpr int NP = D / 64;
-  const long long w = static_cast<long long>(blockIdx.x) * 4 + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
-  const int row = static_cast<int>(w / p.hkv), h = static_cast<int>(w % p.hkv);
-  if (row >= p.total_rows || row >= p.q_start[p.batch]) return;
-  int b = 0, e = p.batch;
-  while (e - b > 1) {
-    const int mid = (b + e) >> 1;
-    if (p.q_start[mid] <= row) b = mid;
-    else e = mid;
-  }
-  const int i = row - p.q_start[b], n = p.q_start[b + 1] - p.q_start[b];
-  const int L = p.seq_lens[b];
-  bool poison = false;
-  if (L < 0 || L > p.max_len - n) {
-    if (lane == 0) atomicOr(p.status, 2);
-    poison = true;
-  }
-  const int hi = poison ? 0 : L + i + p.self;
-  const int lo = p.window ? max(0, hi - p.window) : 0;
-  const int sk = min(p.sinks, lo);
-  uint64_t tn[NP];
-  float qx[G][NP], qy[G][NP], m[G], l[G], ox[G][NP], oy[G][NP];
-#pragma unroll
-  for (int j = 0; j < NP; ++j) {
-    tn[j] = ROPE ? p.turns[lane + 32 * j] : 0;
-    float c = 1.f, s = 0.f;
-    if (ROPE) turn_cs(L + i, tn[j], c, s);
-#pragma unroll
-    for (int g = 0; g < G; ++g) {
-      const uint16_t* q = p.q + row * p.q_stride + (h * G + g) * D;
-      const float x = widen1<BF16>(q[lane + 32 * j]), y = widen1<BF16>(q[lane + 32 * j + D / 2]);
-      qx[g][j] = (x * c - y * s) * p.qscale;
-      qy[g][j] = (y * c + x * s) * p.qscale;
-      ox[g][j] = oy[g][j] = 0.f;
-      m[g] = -1e30f;
-      l[g] = 0.f;
-    }
-  }
-  for (int t = sk > 0 ? 0 : lo; t < hi; t = t + 1 == sk ? lo : t + 1) {
-    const int blk = t / p.block_size;
-    const int id = p.table[static_cast<size_t>(b) * p.stride + blk];
-    if (id < 0 || id >= p.id_total) {
-      if (lane == 0) atomicOr(p.status, 1);
-      poison = true;
-      break;
-    }
-    const bool host = id < p.host_split;
-    const size_t at = ((static_cast<size_t>(host ? id : id - p.host_split) * p.hkv + h) * p.block_size +
-                       (t - blk * p.block_size)) * D;
-    const uint16_t* k = (host ? p.k_host : p.k_dev) + at;
-    const uint16_t* v = (host ? p.v_host : p.v_dev) + at;
-    float sc[G];
-#pragma unroll
-    for (int g = 0; g < G; ++g) sc[g] = 0.f;
-#pragma unroll
-    for (int j = 0; j < NP; ++j) {
-      const float x = widen1<BF16>(k[lane + 32 * j]), y = widen1<BF16>(k[lane + 32 * j + D / 2]);
-      float c = 1.f, s = 0.f;
-      if (ROPE) turn_cs(t, tn[j], c, s);
-      const float kx = x * c - y * s, ky = y * c + x * s;
-#pragma unroll
-      for (int g = 0; g < G; ++g) sc[g] = fmaf(qx[g][j], kx, fmaf(qy[g][j], ky, sc[g]));
-    }
-#pragma unroll
-    for (int g = 0; g < G; ++g) {
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) sc[g] += __shfl_xor_sync(kFull, sc[g], o);
-      const float mx = fmaxf(m[g], sc[g]);
-      const float a = exp2f(m[g] - mx), pw = exp2f(sc[g] - mx);
-      m[g] = mx;
-      l[g] = l[g] * a + pw;
-#pragma unroll
-      for (int j = 0; j < NP; ++j) {
-        ox[g][j] = ox[g][j] * a + pw * widen1<BF16>(v[lane + 32 * j]);
-        oy[g][j] = oy[g][j] * a + pw * widen1<BF16>(v[lane + 32 * j + D / 2]);
+// max(|a|, |b|) of fp16 pairs; a NaN is ignored.
+__device__ __forceinline__ uint32_t hmax_abs2(uint32_t m, uint32_t v) {
+  const uint32_t a = v & 0x7fff7fffu;
+  const __half2 r = __hmax2(*reinterpret_cast<const __half2*>(&m), *reinterpret_cast<const __half2*>(&a));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+__device__ __forceinline__ bool has_inf2(uint32_t m) { return (m & 0xffffu) == 0x7c00u || (m >> 16) == 0x7c00u; }
+
+// A wait of the chunk kernel: bounded, and given up as soon as another role has.
+__device__ __forceinline__ bool chunk_wait(uint64_t* bar, uint32_t parity, ChunkTail& t, int32_t* status) {
+  const uint32_t b = smem_u32(bar);
+  if (mbar_try_wait(b, parity)) return true;
+  const unsigned long long t0 = global_ns();
+  for (unsigned i = 1;; ++i) {
+    if (mbar_try_wait(b, parity)) return true;
+    if ((i & 63u) == 0) {
+      if (*reinterpret_cast<volatile int32_t*>(&t.broken)) return false;
+      if (global_ns() - t0 > kWaitLimitNs) {
+        *reinterpret_cast<volatile int32_t*>(&t.broken) = 1;
+        atomicOr(status, kStatusTimeout);
+        return false;
       }
     }
   }
-#pragma unroll
-  for (int g = 0; g < G; ++g) {
-    const float inv = poison ? __int_as_float(0x7fc00000) : (l[g] > 0.f || isnan(l[g]) ? 1.f / l[g] : 0.f);
-    uint16_t* o = p.out + (static_cast<size_t>(row) * p.hq + h * G + g) * D;
-#pragma unroll
-    for (int j = 0; j < NP; ++j) {
-      o[lane + 32 * j] = narrow1<BF16>(ox[g][j] * inv);
-      o[lane + 32 * j + D / 2] = narrow1<BF16>(oy[g][j] * inv);
+}
+
+// Ring position: stage and the parity of its current use.
+struct Ring {
+  int stage = 0;
+  uint32_t parity = 0;
+  template <int N>
+  __device__ __forceinline__ void next() {
+    if (++stage == N) {
+      stage = 0;
+      parity ^= 1u;
     }
   }
+};
+
+// ----------------------------------------------------------------------------- the kernel
+
+template <int D, bool BF16, bool ROPE>
+__global__ void __launch_bounds__(kChunkThreads, 1)
+    chunk_kernel(const ChunkParams p, const __grid_constant__ ChunkMaps maps) {
+  using C = ChunkShape<D>;
+  constexpr bool kOpBf16 = BF16 && !ROPE;    // type of the Q K^T operands
+  extern __shared__ __align__(1024) char chunk_smem[];
+  char* const sq = chunk_smem;
+  char* const sk = sq + 2 * C::kTile;
+  char* const sv = sk + C::kStagesK * C::kTile;
+  ChunkTail& t = *reinterpret_cast<ChunkTail*>(sv + C::kStagesV * C::kTile);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  if (smem_u32(chunk_smem) & 1023u) {   // the swizzled tiles need a 1024-byte aligned base
+    if (tid == 0) atomicOr(p.status, kStatusLayout);
+    return;
+  }
+
+  // ---- which rows: CTA = (row tile, kv head, split), the row tiles counted
+  // from the last one of the last sequence, as the last rows of a chunk see
+  // the most tokens
+  const int unit = p.div_split.div(static_cast<int>(blockIdx.x));
+  const int split = static_cast<int>(blockIdx.x) - unit * p.nsplit;
+  const int slot = p.div_hkv.div(unit);
+  const int h = unit - slot * p.hkv;
+  if (warp == 0) {
+    int before = 0, fb = -1, ft = 0;
+    for (int b0 = p.batch - 1; b0 >= 0 && fb < 0; b0 -= 32) {
+      const int b = b0 - lane;
+      const int n = b >= 0 ? p.q_start[b + 1] - p.q_start[b] : 0;
+      const int tiles = n > 0 ? static_cast<int>(((static_cast<long long>(n) << p.group_shift) + kChunkRows - 1) / kChunkRows) : 0;
+      int inc = tiles;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(kFull, inc, o);
+        if (lane >= o) inc += u;
+      }
+      const unsigned hit = __ballot_sync(kFull, slot < before + inc && slot >= before + inc - tiles);
+      if (hit) {
+        const int src = __ffs(hit) - 1;
+        fb = b0 - src;
+        ft = __shfl_sync(kFull, before + inc - 1 - slot, src);
+      }
+      before += __shfl_sync(kFull, inc, 31);
+    }
+    if (lane == 0) {
+      t.b = fb;
+      t.tile = ft;
+      t.poison = 0;
+      t.broken = 0;
+    }
+  }
+  __syncthreads();
+  const int b = t.b;
+  if (b < 0) return;
+  const int q0 = p.q_start[b];
+  const int n = p.q_start[b + 1] - q0;
+  const int L = p.seq_lens[b];
+  const int row0 = t.tile * kChunkRows;
+  const int rows = min((n << p.group_shift) - row0, kChunkRows);
+  const int num_m = rows > 128 ? 2 : 1;
+  const bool bad_len = L < 0 || L > p.max_len - n;
+
+  // ---- which tokens: [0, sk_end) and [lo_min, hi_max), in tiles of 128
+  const int hi_min = L + (row0 >> p.group_shift) + p.self;
+  const int hi_max = L + ((row0 + rows - 1) >> p.group_shift) + p.self;
+  const int lo_min = p.window ? max(0, hi_min - p.window) : 0;
+  const int sk_end = min(p.sinks, lo_min);
+  const int tb = lo_min / kChunkTokens;
+  const int na = min((sk_end + kChunkTokens - 1) / kChunkTokens, tb);
+  const int total = bad_len ? 0 : na + max(0, (hi_max + kChunkTokens - 1) / kChunkTokens - tb);
+  const int per = (total + p.nsplit - 1) / p.nsplit;
+  const int j0 = min(split * per, total);
+  const int nt = min(j0 + per, total) - j0;
+  auto tile_pos = [&](int j) { return (j0 + j < na ? j0 + j : tb + j0 + j - na) * kChunkTokens; };
+
+  // output of this thread's row (softmax warps: row tile `m`)
+  const int m = (warp >> 2) - 2;                 // softmax: row tile 0 or 1
+  const int idx = row0 + (tid & 255);            // threads 256..511 own rows 0..255
+  const int tok = idx >> p.group_shift;
+  const int head = (h << p.group_shift) + (idx & ((1 << p.group_shift) - 1));
+  const long long row = static_cast<long long>(q0) + tok;
+  const bool live = m >= 0 && tok < n && row >= 0 && row < p.total_rows;
+
+  if (nt == 0 || p.id_total == 0) {
+    // no token to see: zero rows; an invalid length, or no pool to look in: NaN rows
+    const bool nan = bad_len || (p.id_total == 0 && total > 0);
+    if (nan && tid == 0) atomicOr(p.status, bad_len ? 2 : 1);
+    if (live) {
+      const size_t at = static_cast<size_t>(row) * p.hq + head;
+      if (p.nsplit == 1) {
+        const uint32_t f = nan ? 0x7fff7fffu : 0u;
+        for (int c = 0; c < D / 8; ++c) reinterpret_cast<uint4*>(p.out + at * D)[c] = make_uint4(f, f, f, f);
+      } else {
+        const float f = nan ? __int_as_float(0x7fc00000) : 0.f;
+        float4* o = reinterpret_cast<float4*>(p.part_o + (at * p.nsplit + split) * D);
+        for (int c = 0; c < D / 4; ++c) o[c] = make_float4(f, f, f, f);
+        p.part_lse[at * p.nsplit + split] = nan ? f : -INFINITY;
+      }
+    }
+    return;
+  }
+
+  if (warp == 1) {
+    if (lane == 0) {
+      for (int i = 0; i < 4; ++i) {
+        mbar_init(smem_u32(&t.k_full[i]), 1);
+        mbar_init(smem_u32(&t.k_ready[i]), 4);
+        mbar_init(smem_u32(&t.k_free[i]), 1);
+        mbar_init(smem_u32(&t.v_full[i]), 1);
+        mbar_init(smem_u32(&t.v_free[i]), 1);
+      }
+      for (int i = 0; i < 2; ++i) {
+        mbar_init(smem_u32(&t.q_ready[i]), 4);
+        mbar_init(smem_u32(&t.s_full[i]), 1);
+        mbar_init(smem_u32(&t.p_ready[i]), 4);
+      }
+      mbar_init(smem_u32(&t.done), 1);
+      mbar_init_fence();
+    }
+    __syncwarp();
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&t.tmem))
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  tmem_fence_before();
+  __syncthreads();
+  tmem_fence_after();
+  const uint32_t tmem = t.tmem;
+  // TMEM columns: S (and P over its first half) of row tile i at 128 i, O at 256 + D i
+
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
+    if (warp == 0) {
+      // ------------------------------------------------------------ copies
+      Ring rk, rv;
+      const int nbox = kChunkTokens / p.box;
+      const uint32_t box_bytes = static_cast<uint32_t>(p.box) * 128;
+      const int32_t* trow = p.table + static_cast<size_t>(b) * p.stride;
+      for (int j = 0; j < nt; ++j) {
+        // the run of rows this lane copies: block, pool and row, or a row that fills with zeros
+        int y = p.oob_row;
+        bool host = p.oob_host != 0;
+        if (lane < nbox) {
+          const int t0 = tile_pos(j) + lane * p.box;
+          if (t0 < hi_max && (t0 + p.box > lo_min || t0 < sk_end)) {
+            const int blk = p.div_bs.div(t0);
+            const int id = trow[blk];
+            if (id >= 0 && id < p.id_total) {
+              host = id < p.host_split;
+              y = ((host ? id : id - p.host_split) * p.hkv + h) * p.block_size + (t0 - blk * p.block_size);
+            } else {
+              *reinterpret_cast<volatile int32_t*>(&t.poison) = 1;
+              atomicOr(p.status, 1);
+            }
+          }
+        }
+        __syncwarp();
+        if (!__all_sync(kFull, chunk_wait(&t.k_free[rk.stage], rk.parity ^ 1u, t, p.status))) break;
+        const uint32_t kb = smem_u32(&t.k_full[rk.stage]);
+        if (lane == 0) mbar_arrive_expect_tx(kb, C::kTile);
+        __syncwarp();
+        if (lane < nbox) {
+          const uint32_t dst = smem_u32(sk + rk.stage * C::kTile) + lane * box_bytes;
+#pragma unroll
+          for (int x = 0; x < C::kSub; ++x)
+            tma_load_2d(dst + x * kSubTile, host ? &maps.k_host : &maps.k_dev, 64 * x, y, kb);
+        }
+        rk.next<C::kStagesK>();
+        if (!__all_sync(kFull, chunk_wait(&t.v_free[rv.stage], rv.parity ^ 1u, t, p.status))) break;
+        const uint32_t vb = smem_u32(&t.v_full[rv.stage]);
+        if (lane == 0) mbar_arrive_expect_tx(vb, C::kTile);
+        __syncwarp();
+        if (lane < nbox) {
+          const uint32_t dst = smem_u32(sv + rv.stage * C::kTile) + lane * box_bytes;
+#pragma unroll
+          for (int x = 0; x < C::kSub; ++x)
+            tma_load_2d(dst + x * kSubTile, host ? &maps.v_host : &maps.v_dev, 64 * x, y, vb);
+        }
+        rv.next<C::kStagesV>();
+      }
+      // copies still in flight after a wait ran out get a bounded time to land
+      // before the block's shared memory is released (a barrier's completed
+      // phase is the parity before the next use's)
+      if (*reinterpret_cast<volatile int32_t*>(&t.broken)) {
+        Ring ek = rk, ev = rv;
+        for (int i = 0; i < C::kStagesK; ++i, ek.next<C::kStagesK>())
+          mbar_wait_bounded(smem_u32(&t.k_full[ek.stage]), ek.parity ^ 1u);
+        for (int i = 0; i < C::kStagesV; ++i, ev.next<C::kStagesV>())
+          mbar_wait_bounded(smem_u32(&t.v_full[ev.stage]), ev.parity ^ 1u);
+      }
+    } else if (warp == 1) {
+      // ------------------------------------------------------------ matrix products
+      constexpr uint32_t kIdQK = umma_idesc(128, kChunkTokens, kOpBf16, false);
+      constexpr uint32_t kIdPV = umma_idesc(128, D, BF16, true);
+      auto qk = [&](int mt, int stage) {   // S = Q K^T: both K-major, 8-row groups 1024 bytes apart
+        const uint32_t a = smem_u32(sq + mt * C::kTile), k = smem_u32(sk + stage * C::kTile);
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) {
+          const uint32_t o = (i >> 2) * kSubTile + (i & 3) * 32;
+          umma_ss(tmem + 128 * mt, umma_desc(a + o, 16, 1024), umma_desc(k + o, 16, 1024), kIdQK, i > 0);
+        }
+        umma_commit(smem_u32(&t.s_full[mt]));
+      };
+      auto pv = [&](int mt, int stage, bool acc) {   // O += P V: V is N-major, 64-column blocks kSubTile apart
+        const uint32_t v = smem_u32(sv + stage * C::kTile);
+#pragma unroll
+        for (int i = 0; i < kChunkTokens / 16; ++i)
+          umma_ts(tmem + 256 + D * mt, tmem + 128 * mt + 8 * i, umma_desc(v + i * 2048, kSubTile, 1024), kIdPV,
+                  acc || i > 0);
+      };
+      Ring rk, rv;
+      bool ok = true;
+      for (int i = 0; i < num_m; ++i) ok = ok && chunk_wait(&t.q_ready[i], 0, t, p.status);
+      ok = ok && chunk_wait(&t.k_ready[0], 0, t, p.status);
+      if (__all_sync(kFull, ok)) {
+        tmem_fence_after();
+        if (lane == 0) {
+          for (int i = 0; i < num_m; ++i) qk(i, 0);
+          umma_commit(smem_u32(&t.k_free[0]));
+        }
+        rk.next<C::kStagesK>();
+        for (int j = 0; j < nt; ++j) {
+          const bool more = j + 1 < nt;
+          ok = __all_sync(kFull, chunk_wait(&t.v_full[rv.stage], rv.parity, t, p.status));
+          for (int i = 0; i < num_m && ok; ++i) {
+            ok = chunk_wait(&t.p_ready[i], j & 1, t, p.status);
+            if (i == 0 && more) ok = ok && chunk_wait(&t.k_ready[rk.stage], rk.parity, t, p.status);
+            if (!(ok = __all_sync(kFull, ok))) break;
+            tmem_fence_after();
+            if (lane == 0) {
+              pv(i, rv.stage, j > 0);
+              if (i == num_m - 1) umma_commit(smem_u32(&t.v_free[rv.stage]));
+              if (more) {
+                qk(i, rk.stage);
+                if (i == num_m - 1) umma_commit(smem_u32(&t.k_free[rk.stage]));
+              }
+            }
+            __syncwarp();
+          }
+          if (!ok) break;
+          rv.next<C::kStagesV>();
+          rk.next<C::kStagesK>();
+        }
+      }
+      // also after a wait ran out: what was issued completes before TMEM is given back
+      if (lane == 0) umma_commit(smem_u32(&t.done));
+      __syncwarp();
+      mbar_wait_bounded(smem_u32(&t.done), 0);
+    }
+  } else if (warp < 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRotate));
+    // -------------------------------------------------------------- rotation of K, in place
+    // A thread owns 8 consecutive pairs (one 16-byte chunk of each half) of
+    // every kStep-th row; its cos / sin advance kStep positions from row to
+    // row, across tiles too while positions continue, with a fresh seed at
+    // least every kRopeChain tiles (64 fp32 steps at most, 2^-18).
+    constexpr int kChunks = D / 16;             // chunks of a half row
+    constexpr int kStep = 128 / kChunks;
+    const int r = tid - 128;
+    const int c = r % kChunks, rr = r / kChunks;
+    float2 E[4], F[4], Cc[4], Sc[4];
+    if constexpr (ROPE) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        turn_cs(kStep, p.turns[8 * c + 2 * i], E[i].x, F[i].x);
+        turn_cs(kStep, p.turns[8 * c + 2 * i + 1], E[i].y, F[i].y);
+      }
+    }
+    int next_pos = -1, chain = 0;
+    Ring rk, rv;
+    for (int j = 0; j < nt; ++j) {
+      const int p0 = tile_pos(j);
+      const bool edge = p0 + kChunkTokens > hi_max || (p0 < lo_min && p0 + kChunkTokens > sk_end);
+      if constexpr (ROPE) {
+        if (p0 != next_pos || chain == kRopeChain) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            turn_cs(p0 + rr, p.turns[8 * c + 2 * i], Cc[i].x, Sc[i].x);
+            turn_cs(p0 + rr, p.turns[8 * c + 2 * i + 1], Cc[i].y, Sc[i].y);
+          }
+          chain = 0;
+        }
+        ++chain;
+        next_pos = p0 + kChunkTokens;
+      }
+      if (!__all_sync(kFull, chunk_wait(&t.k_full[rk.stage], rk.parity, t, p.status))) break;
+      if constexpr (ROPE) {
+        char* const k = sk + rk.stage * C::kTile;
+        uint32_t mx = 0;
+#pragma unroll
+        for (int i = 0; i < 128 / kStep; ++i) {
+          const int rw = rr + kStep * i;
+          uint4* const px = reinterpret_cast<uint4*>(k + rw * 128 + ((c ^ (rw & 7)) << 4));
+          uint4* const py = D == 128 ? px + kSubTile / 16
+                                     : reinterpret_cast<uint4*>(k + rw * 128 + (((c + 4) ^ (rw & 7)) << 4));
+          const uint4 ux = *px, uy = *py;
+          float2 X[4] = {widen2<BF16>(ux.x), widen2<BF16>(ux.y), widen2<BF16>(ux.z), widen2<BF16>(ux.w)};
+          float2 Y[4] = {widen2<BF16>(uy.x), widen2<BF16>(uy.y), widen2<BF16>(uy.z), widen2<BF16>(uy.w)};
+          rope_rotate_advance<4>(X, Y, Cc, Sc, E, F);
+          uint32_t o[8];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            o[e] = narrow2<false>(X[e].x, X[e].y);
+            o[4 + e] = narrow2<false>(Y[e].x, Y[e].y);
+          }
+          // range: only of tokens that some row sees, the others hold anything
+          const int tt = p0 + rw;
+          if (!edge || (tt < hi_max && (tt >= lo_min || tt < sk_end))) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) mx = hmax_abs2(mx, o[e]);
+          }
+          *px = make_uint4(o[0], o[1], o[2], o[3]);
+          *py = make_uint4(o[4], o[5], o[6], o[7]);
+        }
+        if (has_inf2(mx)) {
+          *reinterpret_cast<volatile int32_t*>(&t.poison) = 1;
+          atomicOr(p.status, kStatusRange);
+        }
+      }
+      if (edge) {
+        // V rows that no row sees: their weights are 0, but 0 * NaN is not
+        if (!__all_sync(kFull, chunk_wait(&t.v_full[rv.stage], rv.parity, t, p.status))) break;
+        const int tt = p0 + r;
+        if (tt >= hi_max || (tt < lo_min && tt >= sk_end)) {
+          char* const v = sv + rv.stage * C::kTile + r * 128;
+#pragma unroll
+          for (int e = 0; e < 8 * C::kSub; ++e)
+            *reinterpret_cast<uint4*>(v + (e >> 3) * kSubTile + (e & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+        }
+      }
+      fence_proxy_async();   // the products read what was written here
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&t.k_ready[rk.stage]));
+      rk.next<C::kStagesK>();
+      rv.next<C::kStagesV>();
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
+    // -------------------------------------------------------------- softmax, a thread per row
+    const int r = tid & 127;
+    if (m < num_m) {
+      // the row's query: rotated, to its place in the swizzled tile; rows past the end are zero
+      const int pos = L + tok;
+      {
+        const uint16_t* const qr = p.q + (live ? row : 0) * p.q_stride + static_cast<size_t>(head) * D;
+        char* const dst = sq + m * C::kTile + r * 128;
+        uint32_t mx = 0;
+#pragma unroll 1
+        for (int c = 0; c < D / 16; ++c) {
+          uint4 ux = make_uint4(0u, 0u, 0u, 0u), uy = ux;
+          if (live) {
+            ux = *reinterpret_cast<const uint4*>(qr + 8 * c);
+            uy = *reinterpret_cast<const uint4*>(qr + D / 2 + 8 * c);
+          }
+          if constexpr (ROPE) {
+            const uint32_t wx[4] = {ux.x, ux.y, ux.z, ux.w}, wy[4] = {uy.x, uy.y, uy.z, uy.w};
+            uint32_t o[8];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float2 x = widen2<BF16>(wx[e]), y = widen2<BF16>(wy[e]);
+              float c0, s0, c1, s1;
+              turn_cs(pos, p.turns[8 * c + 2 * e], c0, s0);
+              turn_cs(pos, p.turns[8 * c + 2 * e + 1], c1, s1);
+              o[e] = narrow2<false>(x.x * c0 - y.x * s0, x.y * c1 - y.y * s1);
+              o[4 + e] = narrow2<false>(y.x * c0 + x.x * s0, y.y * c1 + x.y * s1);
+              mx = hmax_abs2(hmax_abs2(mx, o[e]), o[4 + e]);
+            }
+            ux = make_uint4(o[0], o[1], o[2], o[3]);
+            uy = make_uint4(o[4], o[5], o[6], o[7]);
+          }
+          *reinterpret_cast<uint4*>(dst + ((c ^ (r & 7)) << 4)) = ux;
+          if constexpr (D == 128) *reinterpret_cast<uint4*>(dst + kSubTile + ((c ^ (r & 7)) << 4)) = uy;
+          else *reinterpret_cast<uint4*>(dst + (((c + 4) ^ (r & 7)) << 4)) = uy;
+        }
+        if (has_inf2(mx)) {
+          *reinterpret_cast<volatile int32_t*>(&t.poison) = 1;
+          atomicOr(p.status, kStatusRange);
+        }
+        fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&t.q_ready[m]));
+      }
+      const int hi = live ? pos + p.self : 0;
+      const int lo = p.window ? max(0, hi - p.window) : 0;
+      // the row tile's tightest bounds: a K/V tile inside them needs no mask
+      const int first = L + ((row0 + 128 * m) >> p.group_shift) + p.self;
+      const int last = L + ((row0 + min(rows, 128 * m + 128) - 1) >> p.group_shift) + p.self;
+      const int lo_last = p.window ? max(0, last - p.window) : 0;
+      const bool full_tile = rows >= 128 * m + 128;
+      const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+      const uint32_t ts = tmem + lanes + 128 * m, to = tmem + lanes + 256 + D * m;
+      float ref = -1e30f, sum = 0.f;
+      bool ok = true;
+      for (int j = 0; j < nt; ++j) {
+        const int p0 = tile_pos(j);
+        ok = __all_sync(kFull, chunk_wait(&t.s_full[m], j & 1, t, p.status));
+        if (!ok) break;
+        tmem_fence_after();
+        uint32_t s[4][32];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) tmem_ld32(ts + 32 * i, s[i]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) tmem_ld_wait(s[i]);
+        if (!full_tile || p0 + kChunkTokens > first || (p0 < lo_last && p0 + kChunkTokens > p.sinks)) {
+          const int h1 = hi - p0, l1 = lo - p0, s1 = p.sinks - p0;
+#pragma unroll
+          for (int i = 0; i < 128; ++i)
+            if (i >= h1 || (i < l1 && i >= s1)) s[i >> 5][i & 31] = 0xff800000u;   // -inf
+        }
+        float mx[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          mx[i] = __uint_as_float(s[i][0]);
+#pragma unroll
+          for (int e = 1; e < 32; ++e) mx[i] = fmaxf(mx[i], __uint_as_float(s[i][e]));
+        }
+        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.qscale;
+        // a higher reference, once some score exceeds the old one by 2^8
+        const bool raise = top > ref + kLazyMax;
+        if (__any_sync(kFull, raise)) {
+          const float now = raise ? top : ref;
+          const float a = ex2(ref - now);
+          ref = now;
+          sum *= a;
+          if (j > 0) {   // the product that last added to O has completed: it precedes this S
+#pragma unroll 1
+            for (int i = 0; i < D / 32; ++i) {
+              uint32_t o[32];
+              tmem_ld32(to + 32 * i, o);
+              tmem_ld_wait(o);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * a);
+              tmem_st32(to + 32 * i, o);
+            }
+          }
+        }
+        const float2 sc = f2(p.qscale), off = f2(-ref);
+        float2 acc[2] = {f2(0.f), f2(0.f)};
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          uint32_t w[32];
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            const uint32_t* const v = s[2 * i + (e >> 4)] + 2 * (e & 15);
+            const float2 x = __ffma2_rn(make_float2(__uint_as_float(v[0]), __uint_as_float(v[1])), sc, off);
+            const float2 y = make_float2(ex2(x.x), ex2(x.y));
+            acc[e & 1] = __fadd2_rn(acc[e & 1], y);
+            w[e] = narrow2<BF16>(y.x, y.y);
+          }
+          tmem_st32(ts + 32 * i, w);
+        }
+        sum += (acc[0].x + acc[0].y) + (acc[1].x + acc[1].y);
+        tmem_st_wait();
+        tmem_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&t.p_ready[m]));
+      }
+      ok = ok && __all_sync(kFull, chunk_wait(&t.done, 0, t, p.status));
+      tmem_fence_after();
+      // ---- the row's result
+      const bool nan = !ok || *reinterpret_cast<volatile int32_t*>(&t.poison);
+      const float inv = nan ? __int_as_float(0x7fc00000) : (sum == 0.f ? 0.f : 1.f / sum);
+      const size_t at = static_cast<size_t>(live ? row : 0) * p.hq + head;
+#pragma unroll 1
+      for (int i = 0; i < D / 32; ++i) {
+        uint32_t o[32];
+        tmem_ld32(to + 32 * i, o);
+        tmem_ld_wait(o);
+        if (live && p.nsplit == 1) {
+          uint4* const dst = reinterpret_cast<uint4*>(p.out + at * D + 32 * i);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            uint32_t w[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              w[k] = narrow2<BF16>(__uint_as_float(o[8 * e + 2 * k]) * inv, __uint_as_float(o[8 * e + 2 * k + 1]) * inv);
+            dst[e] = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        } else if (live) {
+          float4* const dst = reinterpret_cast<float4*>(p.part_o + (at * p.nsplit + split) * D + 32 * i);
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            dst[e] = make_float4(__uint_as_float(o[4 * e]) * inv, __uint_as_float(o[4 * e + 1]) * inv,
+                                 __uint_as_float(o[4 * e + 2]) * inv, __uint_as_float(o[4 * e + 3]) * inv);
+        }
+        __syncwarp();
+      }
+      if (live && p.nsplit > 1)
+        p.part_lse[at * p.nsplit + split] = nan ? __int_as_float(0x7fc00000) : (sum == 0.f ? -INFINITY : ref + __log2f(sum));
+    }
+  }
+  tmem_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tmem_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+  }
+}
+
+// ----------------------------------------------------------------------------- joining the splits
+
+// One warp per (row, head): o = sum_i 2^(lse_i - top) o_i / sum_i 2^(lse_i - top).
+// A NaN split makes the row NaN; a row whose splits are all empty is zero.
+template <int D, bool BF16>
+__global__ void __launch_bounds__(128) chunk_merge_kernel(const ChunkParams p) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const long long w = static_cast<long long>(blockIdx.x) * 4 + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  if (w >= static_cast<long long>(min(p.total_rows, p.q_start[p.batch])) * p.hq) return;
+  const float* const lse = p.part_lse + w * p.nsplit;
+  const float* const o = p.part_o + w * p.nsplit * D;
+  float top = -INFINITY;
+  bool nan = false;
+  for (int i = lane; i < p.nsplit; i += 32) {
+    const float l = lse[i];
+    nan |= isnan(l);
+    top = fmaxf(top, l);
+  }
+#pragma unroll
+  for (int k = 16; k > 0; k >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, k));
+  nan = __any_sync(kFull, nan);
+  float z = 0.f, acc[D / 32];
+#pragma unroll
+  for (int k = 0; k < D / 32; ++k) acc[k] = 0.f;
+  if (top != -INFINITY) {
+    for (int i = 0; i < p.nsplit; ++i) {
+      const float f = ex2(lse[i] - top);
+      z += f;
+#pragma unroll
+      for (int k = 0; k < D / 64; ++k) {
+        const float2 x = *reinterpret_cast<const float2*>(o + static_cast<size_t>(i) * D + 64 * k + 2 * lane);
+        acc[2 * k] = fmaf(f, x.x, acc[2 * k]);
+        acc[2 * k + 1] = fmaf(f, x.y, acc[2 * k + 1]);
+      }
+    }
+  }
+  const float inv = nan ? __int_as_float(0x7fc00000) : (z > 0.f ? 1.f / z : 0.f);
+#pragma unroll
+  for (int k = 0; k < D / 64; ++k)
+    *reinterpret_cast<uint32_t*>(p.out + w * D + 64 * k + 2 * lane) = narrow2<BF16>(acc[2 * k] * inv, acc[2 * k + 1] * inv);
 }
 
 }  // namespace dkv

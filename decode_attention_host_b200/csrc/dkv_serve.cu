@@ -13,6 +13,7 @@
 #include "dkv_kernels.cuh"
 #include "dkv_plan.h"
 #include "dkv_tables.cuh"
+#include "dkv_tma.h"
 
 namespace {
 
@@ -33,12 +34,35 @@ dkv::SplitEntry window_entry() {
           reinterpret_cast<const void*>(&dkv::split_kernel<D, G, BF16, kWinStages, ROPE, false, true>)};
 }
 
-template <int D, int G, bool BF16, bool ROPE>
-void launch_chunk(cudaStream_t s, const dkv::ChunkParams& p) {
-  const long long warps = static_cast<long long>(p.total_rows) * p.hkv;
-  dkv::chunk_row_kernel<D, G, BF16, ROPE><<<static_cast<unsigned>((warps + 3) / 4), 128, 0, s>>>(p);
+template <int D, bool BF16, bool ROPE>
+cudaError_t launch_chunk(cudaStream_t s, const dkv::ChunkParams& p, const dkv::ChunkMaps& m, int ctas) {
+  dkv::chunk_kernel<D, BF16, ROPE><<<ctas, dkv::kChunkThreads, dkv::chunk_smem_bytes<D>(), s>>>(p, m);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess || p.nsplit == 1) return e;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>((static_cast<long long>(p.total_rows) * p.hq + 3) / 4));
+  cfg.blockDim = dim3(128);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, dkv::chunk_merge_kernel<D, BF16>, p);
 }
-using ChunkFn = void (*)(cudaStream_t, const dkv::ChunkParams&);
+
+template <int D, bool BF16, bool ROPE>
+cudaError_t prepare_chunk() {
+  auto* const k = dkv::chunk_kernel<D, BF16, ROPE>;
+  cudaFuncAttributes a{};
+  cudaError_t e = cudaFuncGetAttributes(&a, k);
+  if (e != cudaSuccess) return e;
+  // the warp groups divide the launch's registers among themselves; with fewer
+  // of them the softmax warps would wait for registers that do not exist
+  if (a.numRegs < dkv::kRegsLaunch) return cudaErrorInvalidKernelImage;
+  return cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              static_cast<int>(dkv::chunk_smem_bytes<D>()));
+}
 
 // Calls f.template operator()<D, G, BF16, ROPE>() for a handle's shape.
 template <class F>
@@ -65,12 +89,41 @@ struct PickWindow {
     return window_entry<D, G, BF16, ROPE>();
   }
 };
-struct PickChunk {
+struct LaunchChunk {
+  cudaStream_t s;
+  const dkv::ChunkParams& p;
+  const dkv::ChunkMaps& m;
+  int ctas;
   template <int D, int G, bool BF16, bool ROPE>
-  ChunkFn operator()() const {
-    return &launch_chunk<D, G, BF16, ROPE>;
+  cudaError_t operator()() const {
+    return launch_chunk<D, BF16, ROPE>(s, p, m, ctas);
   }
 };
+struct PrepareChunk {
+  template <int D, int G, bool BF16, bool ROPE>
+  cudaError_t operator()() const {
+    return prepare_chunk<D, BF16, ROPE>();
+  }
+};
+
+// Splits of every row tile's walk over the cache.  A CTA takes one (row tile,
+// kv head, split) and holds its SM; the time is the number of waves times a
+// CTA's share of the walk, plus about 3 tiles' time for its start and end and,
+// with splits, as much again for joining them.  `tiles` goes by the table's
+// capacity, as the lengths are on the device.
+int chunk_splits(long long units, int sms, long long tiles, long long max_splits) {
+  int best = 1;
+  double best_cost = 0.0;
+  for (int n = 1; n <= 64 && n <= max_splits && (n == 1 || 2 * n <= tiles); ++n) {
+    const double waves = static_cast<double>((units * n + sms - 1) / sms);
+    const double cost = waves * (static_cast<double>((tiles + n - 1) / n) + 3.0) + (n > 1 ? 3.0 : 0.0);
+    if (n == 1 || cost < 0.97 * best_cost) {
+      best = n;
+      best_cost = cost;
+    }
+  }
+  return best;
+}
 
 // The checks of the two attention entry points that do not depend on the
 // query layout: batch, table, ids, pools (aligned, and of the right kind).
@@ -111,6 +164,8 @@ cudaError_t dkv::prepare_serving(dkv_handle* h) {
   if (e != cudaSuccess) return e;
   e = cudaFuncSetAttribute(h->window_kernel.ptr, cudaFuncAttributePreferredSharedMemoryCarveout,
                            cudaSharedmemCarveoutMaxShared);
+  if (e != cudaSuccess) return e;
+  e = by_shape(h->cfg, PrepareChunk{});
   if (e != cudaSuccess) return e;
   return cudaFuncSetAttribute(extend_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                               static_cast<int>(table_smem_bytes(kTableMaxBatch)));
@@ -213,7 +268,8 @@ int dkv_attn_chunk(dkv_handle* h, const void* q, int64_t q_stride, const int32_t
   if (!h) return set_error(DKV_ERR_INVALID_ARG, "dkv_attn_chunk: null handle");
   const dkv_config& c = h->cfg;
   if (batch < 0 || batch > c.max_batch) return set_error(DKV_ERR_INVALID_ARG, "dkv_attn_chunk: batch outside [0, max_batch]");
-  if (total_rows < 0) return set_error(DKV_ERR_INVALID_ARG, "dkv_attn_chunk: total_rows < 0");
+  if (total_rows < 0 || total_rows > (1 << 28))
+    return set_error(DKV_ERR_INVALID_ARG, "dkv_attn_chunk: total_rows outside [0, 2^28]");
   int rc = check_mask("dkv_attn_chunk", window, sinks, include_self, 0);
   if (rc != DKV_OK) return rc;
   if (batch == 0 || total_rows == 0) {
@@ -248,14 +304,12 @@ int dkv_attn_chunk(dkv_handle* h, const void* q, int64_t q_stride, const int32_t
   dkv::ChunkParams p{};
   p.q = static_cast<const uint16_t*>(q);
   p.out = static_cast<uint16_t*>(out);
-  p.k_host = static_cast<const uint16_t*>(k_host);
-  p.v_host = static_cast<const uint16_t*>(v_host);
-  p.k_dev = static_cast<const uint16_t*>(k_dev);
-  p.v_dev = static_cast<const uint16_t*>(v_dev);
   p.q_start = q_start;
   p.seq_lens = seq_lens;
   p.table = block_table;
   p.turns = reinterpret_cast<const uint64_t*>(h->inv_freq + c.head_dim / 2);
+  p.part_o = h->part_o;
+  p.part_lse = h->part_lse;
   p.status = h->status;
   p.q_stride = q_stride;
   p.total_rows = total_rows;
@@ -266,14 +320,41 @@ int dkv_attn_chunk(dkv_handle* h, const void* q, int64_t q_stride, const int32_t
   p.block_size = c.block_size;
   p.host_split = host_split;
   p.id_total = host_split + num_dev_blocks;
-  p.max_len = (block_table_stride < c.max_blocks_per_seq ? block_table_stride : c.max_blocks_per_seq) * c.block_size;
+  const int nblk = block_table_stride < c.max_blocks_per_seq ? block_table_stride : c.max_blocks_per_seq;
+  p.max_len = nblk * c.block_size;
+  p.group_shift = h->G == 4 ? 2 : h->G - 1;
+  p.box = 16;
+  while (p.box < dkv::kChunkTokens && c.block_size % (2 * p.box) == 0) p.box *= 2;
   p.window = window;
   p.sinks = window ? sinks : 0;
   p.self = include_self;
   p.qscale = h->qscale;
-  by_shape(c, PickChunk{})(s, p);
-  DKV_CUDA(cudaGetLastError());
-  h->last_launches = 1;
+  const long long row_tiles = (static_cast<long long>(total_rows) * h->G) / dkv::kChunkRows + batch;
+  const long long units = row_tiles * c.num_kv_heads;
+  long long see = p.max_len;   // tokens that a row tile may walk over
+  if (window && static_cast<long long>(window) + sinks + 2 * dkv::kChunkRows < see)
+    see = static_cast<long long>(window) + sinks + 2 * dkv::kChunkRows;
+  p.nsplit = chunk_splits(units, h->sm_count, (see + dkv::kChunkTokens - 1) / dkv::kChunkTokens,
+                          static_cast<long long>(h->part_rows) / (static_cast<long long>(total_rows) * c.num_q_heads));
+  if (units * p.nsplit > INT_MAX) return set_error(DKV_ERR_INVALID_ARG, "dkv_attn_chunk: too many rows");
+  p.div_bs = dkv::make_invdiv(c.block_size);
+  p.div_hkv = dkv::make_invdiv(c.num_kv_heads);
+  p.div_split = dkv::make_invdiv(p.nsplit);
+  dkv::ChunkMaps maps{};
+  const long long block_rows = static_cast<long long>(c.num_kv_heads) * c.block_size;
+  const long long host_rows = host_split * block_rows, dev_rows = num_dev_blocks * block_rows;
+  if (host_rows >= (1LL << 31) || dev_rows >= (1LL << 31))
+    return set_error(DKV_ERR_INVALID_ARG, "dkv_attn_chunk: a pool holds 2^31 or more token rows");
+  // a pool that is not there is never copied from: its map is the other's
+  p.oob_host = dev_rows == 0;
+  p.oob_row = static_cast<int32_t>(dev_rows ? dev_rows : host_rows);
+  if (!dkv::encode_box_map(&maps.k_dev, dev_rows ? k_dev : k_host, dev_rows ? dev_rows : host_rows, c.head_dim, p.box) ||
+      !dkv::encode_box_map(&maps.v_dev, dev_rows ? v_dev : v_host, dev_rows ? dev_rows : host_rows, c.head_dim, p.box) ||
+      !dkv::encode_box_map(&maps.k_host, host_rows ? k_host : k_dev, host_rows ? host_rows : dev_rows, c.head_dim, p.box) ||
+      !dkv::encode_box_map(&maps.v_host, host_rows ? v_host : v_dev, host_rows ? host_rows : dev_rows, c.head_dim, p.box))
+    return set_error(DKV_ERR_CUDA, "cuTensorMapEncodeTiled rejected the pool's tensor map");
+  DKV_CUDA(by_shape(c, LaunchChunk{s, p, maps, static_cast<int>(units * p.nsplit)}));
+  h->last_launches = p.nsplit > 1 ? 2 : 1;
   return DKV_OK;
 }
 

@@ -58,6 +58,7 @@ extern "C" {
 #define DKV_STATUS_INTERNAL 8     /* the HBM kernel found its shared memory misaligned and did nothing */
 #define DKV_STATUS_NO_FREE_BLOCKS 16 /* dkv_extend_tables: the free list holds too few blocks (nothing was changed) */
 #define DKV_STATUS_NO_SLOTS 32    /* dkv_extend_tables: more new tokens than max_slots (nothing was changed) */
+#define DKV_STATUS_RANGE 64       /* dkv_attn_chunk: a rotated query or key component above 65504; rows that may see it are NaN */
 
 typedef enum { DKV_KV_F16 = 0, DKV_KV_BF16 = 1 } dkv_kv_dtype;
 
@@ -286,8 +287,12 @@ DKV_API int dkv_store_kv(dkv_handle* h, const void* k_new, const void* v_new, in
  *                 host-resident blocks are read in place over PCIe, once for
  *                 every 256 / (Hq/Hkv) rows of a chunk; with them the first
  *                 host_split blocks of the host pools are copied there first.
- * Scores, softmax statistics and outputs are accumulated in fp32.  The stored
- * V rows of tokens that some row of the sequence sees must be finite.
+ * Scores, softmax statistics and outputs are accumulated in fp32; rotated
+ * queries and keys are held in fp16 (|x| <= 65504 after rotation, else
+ * DKV_STATUS_RANGE and NaN for the 256 / (Hq/Hkv) rows of the chunk that are
+ * computed together), softmax weights in the handle's kv_dtype.  A V row that
+ * is not finite spoils the rows that see it, and rows computed together with
+ * those.
  * Errors: INVALID_ARG, CUDA. */
 DKV_API int dkv_attn_chunk(dkv_handle* h, const void* q, int64_t q_stride, const int32_t* q_start,
                            int32_t total_rows, const void* k_host, const void* v_host, const void* k_dev,
