@@ -47,9 +47,9 @@ constexpr int kRopeChain = 8;                      // K tiles that may follow on
 // Registers per thread of the four warp groups, out of the 128 per thread the
 // block is launched with: the shares add up to exactly those.
 constexpr int kRegsLaunch = 128;
-constexpr int kRegsIssue = 48;
+constexpr int kRegsIssue = 64;
 constexpr int kRegsRotate = 96;
-constexpr int kRegsSoftmax = 184;
+constexpr int kRegsSoftmax = 176;
 static_assert(kRegsIssue + kRegsRotate + 2 * kRegsSoftmax <= 4 * kRegsLaunch, "setmaxnreg.inc would wait for ever");
 constexpr int kStatusRange = 64;                   // DKV_STATUS_RANGE
 
@@ -107,12 +107,12 @@ __host__ __device__ constexpr size_t chunk_smem_bytes() {
 
 // ----------------------------------------------------------------------------- tensor core helpers
 
-// Shared-memory matrix descriptor, 128-byte swizzle: start address, the two
-// strides in 16-byte units, descriptor version 1, swizzle mode 2.
-__device__ __forceinline__ uint64_t umma_desc(uint32_t addr, uint32_t lead, uint32_t stride) {
-  return static_cast<uint64_t>((addr >> 4) & 0x3fff) | (static_cast<uint64_t>(lead >> 4) << 16) |
-         (static_cast<uint64_t>(stride >> 4) << 32) | (1ull << 46) | (2ull << 61);
-}
+// Shared-memory matrix descriptor, 128-byte swizzle: start address and the two
+// strides in 16-byte units, descriptor version 1, swizzle mode 2.  Held as its
+// two words: the high one is the same for every operand here (8-row groups
+// 1024 bytes apart), the low one moves by plain additions.
+constexpr uint32_t kDescHigh = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_low(uint32_t addr, uint32_t lead) { return (addr >> 4) | ((lead >> 4) << 16); }
 
 // Instruction descriptor of kind::f16: fp32 accumulator, A and B both fp16 or
 // both bf16, A K-major, B K-major or (mn) N-major.
@@ -121,23 +121,33 @@ __host__ __device__ constexpr uint32_t umma_idesc(int m, int n, bool bf16, bool 
          (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(m >> 4) << 24);
 }
 
-__device__ __forceinline__ void umma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
+// The issuing warp stays converged and one lane's predicate `on` issues: the
+// operands are then warp-uniform values, which the instruction takes from
+// uniform registers, and need no moves there one by one (a branch around the
+// instruction costs those: 97 cycles from one to the next, where the tensor
+// core needs 64).
+__device__ __forceinline__ void umma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool acc, uint32_t on) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc),
-      "r"(static_cast<uint32_t>(acc))
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 a, b;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "mov.b64 a, {%1, %6};\n\tmov.b64 b, {%2, %6};\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(d), "r"(a), "r"(b), "r"(idesc),
+      "r"(static_cast<uint32_t>(acc)), "r"(on), "r"(kDescHigh)
       : "memory");
 }
-__device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool acc) {
+__device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool acc, uint32_t on) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(idesc),
-      "r"(static_cast<uint32_t>(acc))
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 b;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "mov.b64 b, {%2, %6};\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}" ::"r"(d), "r"(a), "r"(b), "r"(idesc),
+      "r"(static_cast<uint32_t>(acc)), "r"(on), "r"(kDescHigh)
       : "memory");
 }
-// One arrival on `bar` when all matrix instructions this thread has issued are complete.
-__device__ __forceinline__ void umma_commit(uint32_t bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+// One arrival on `bar` when all matrix instructions the issuing lane has issued are complete.
+__device__ __forceinline__ void umma_commit(uint32_t bar, uint32_t on) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar), "r"(on)
+      : "memory");
 }
 __device__ __forceinline__ void tmem_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tmem_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
@@ -158,16 +168,25 @@ __device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t (&r)[32]) {
       : "r"(addr)
       : "memory");
 }
-__device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t (&r)[32]) {
+__device__ __forceinline__ void tmem_ld16(uint32_t addr, uint32_t (&r)[16]) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,"
-      "%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::DKV_I8(r, 0), DKV_I8(r, 8), DKV_I8(r, 16),
-      DKV_I8(r, 24), "r"(addr)
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : DKV_O8(r, 0), DKV_O8(r, 8)
+      : "r"(addr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};"
+      ::DKV_I8(r, 0), DKV_I8(r, 8), "r"(addr)
       : "memory");
 }
 // Completes this thread's loads; the registers pass through, so no use of them moves above it.
 __device__ __forceinline__ void tmem_ld_wait(uint32_t (&r)[32]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;" : DKV_R8(r, 0), DKV_R8(r, 8), DKV_R8(r, 16), DKV_R8(r, 24)::"memory");
+}
+__device__ __forceinline__ void tmem_ld_wait(uint32_t (&r)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" : DKV_R8(r, 0), DKV_R8(r, 8)::"memory");
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 #undef DKV_R8
@@ -194,6 +213,9 @@ __device__ __forceinline__ uint32_t narrow2(float x, float y) {
     return *reinterpret_cast<const uint32_t*>(&h);
   }
 }
+
+// The n lowest bits set, n clamped to [0, 32].
+__device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : n >= 32 ? kFull : (1u << n) - 1u; }
 
 // max(|a|, |b|) of fp16 pairs; a NaN is ignored.
 __device__ __forceinline__ uint32_t hmax_abs2(uint32_t m, uint32_t v) {
@@ -246,7 +268,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   char* const sk = sq + 2 * C::kTile;
   char* const sv = sk + C::kStagesK * C::kTile;
   ChunkTail& t = *reinterpret_cast<ChunkTail*>(sv + C::kStagesV * C::kTile);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(kFull, tid >> 5, 0);   // warp-uniform, and known to be
 
   if (smem_u32(chunk_smem) & 1023u) {   // the swizzled tiles need a 1024-byte aligned base
     if (tid == 0) atomicOr(p.status, kStatusLayout);
@@ -430,48 +453,48 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       // ------------------------------------------------------------ matrix products
       constexpr uint32_t kIdQK = umma_idesc(128, kChunkTokens, kOpBf16, false);
       constexpr uint32_t kIdPV = umma_idesc(128, D, BF16, true);
-      auto qk = [&](int mt, int stage) {   // S = Q K^T: both K-major, 8-row groups 1024 bytes apart
-        const uint32_t a = smem_u32(sq + mt * C::kTile), k = smem_u32(sk + stage * C::kTile);
+      const uint32_t on = lane == 0;
+      const int tiles = __shfl_sync(kFull, nt, 0), row_tiles = __shfl_sync(kFull, num_m, 0);
+      const uint32_t tm = __shfl_sync(kFull, tmem, 0);
+      const uint32_t q_low = desc_low(smem_u32(sq), 16), k_low = desc_low(smem_u32(sk), 16);
+      const uint32_t v_low = desc_low(smem_u32(sv), kSubTile);
+      auto qk = [&](int mt, int stage) {   // S = Q K^T, both K-major
+        const uint32_t a = q_low + mt * (C::kTile >> 4), k = k_low + stage * (C::kTile >> 4);
 #pragma unroll
         for (int i = 0; i < D / 16; ++i) {
-          const uint32_t o = (i >> 2) * kSubTile + (i & 3) * 32;
-          umma_ss(tmem + 128 * mt, umma_desc(a + o, 16, 1024), umma_desc(k + o, 16, 1024), kIdQK, i > 0);
+          const uint32_t o = ((i >> 2) * kSubTile + (i & 3) * 32) >> 4;
+          umma_ss(tm + 128 * mt, a + o, k + o, kIdQK, i > 0, on);
         }
-        umma_commit(smem_u32(&t.s_full[mt]));
+        umma_commit(smem_u32(&t.s_full[mt]), on);
       };
       auto pv = [&](int mt, int stage, bool acc) {   // O += P V: V is N-major, 64-column blocks kSubTile apart
-        const uint32_t v = smem_u32(sv + stage * C::kTile);
+        const uint32_t v = v_low + stage * (C::kTile >> 4), pw = tm + 128 * mt;
 #pragma unroll
         for (int i = 0; i < kChunkTokens / 16; ++i)
-          umma_ts(tmem + 256 + D * mt, tmem + 128 * mt + 8 * i, umma_desc(v + i * 2048, kSubTile, 1024), kIdPV,
-                  acc || i > 0);
+          umma_ts(tm + 256 + D * mt, pw + 8 * i, v + i * (2048 >> 4), kIdPV, acc || i > 0, on);
       };
       Ring rk, rv;
       bool ok = true;
-      for (int i = 0; i < num_m; ++i) ok = ok && chunk_wait(&t.q_ready[i], 0, t, p.status);
+      for (int i = 0; i < row_tiles; ++i) ok = ok && chunk_wait(&t.q_ready[i], 0, t, p.status);
       ok = ok && chunk_wait(&t.k_ready[0], 0, t, p.status);
       if (__all_sync(kFull, ok)) {
         tmem_fence_after();
-        if (lane == 0) {
-          for (int i = 0; i < num_m; ++i) qk(i, 0);
-          umma_commit(smem_u32(&t.k_free[0]));
-        }
+        for (int i = 0; i < row_tiles; ++i) qk(i, 0);
+        umma_commit(smem_u32(&t.k_free[0]), on);
         rk.next<C::kStagesK>();
-        for (int j = 0; j < nt; ++j) {
-          const bool more = j + 1 < nt;
+        for (int j = 0; j < tiles; ++j) {
+          const bool more = j + 1 < tiles;
           ok = __all_sync(kFull, chunk_wait(&t.v_full[rv.stage], rv.parity, t, p.status));
-          for (int i = 0; i < num_m && ok; ++i) {
+          for (int i = 0; i < row_tiles && ok; ++i) {
             ok = chunk_wait(&t.p_ready[i], j & 1, t, p.status);
             if (i == 0 && more) ok = ok && chunk_wait(&t.k_ready[rk.stage], rk.parity, t, p.status);
             if (!(ok = __all_sync(kFull, ok))) break;
             tmem_fence_after();
-            if (lane == 0) {
-              pv(i, rv.stage, j > 0);
-              if (i == num_m - 1) umma_commit(smem_u32(&t.v_free[rv.stage]));
-              if (more) {
-                qk(i, rk.stage);
-                if (i == num_m - 1) umma_commit(smem_u32(&t.k_free[rk.stage]));
-              }
+            pv(i, rv.stage, j > 0);
+            if (i == row_tiles - 1) umma_commit(smem_u32(&t.v_free[rv.stage]), on);
+            if (more) {
+              qk(i, rk.stage);
+              if (i == row_tiles - 1) umma_commit(smem_u32(&t.k_free[rk.stage]), on);
             }
             __syncwarp();
           }
@@ -481,8 +504,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         }
       }
       // also after a wait ran out: what was issued completes before TMEM is given back
-      if (lane == 0) umma_commit(smem_u32(&t.done));
-      __syncwarp();
+      umma_commit(smem_u32(&t.done), on);
       mbar_wait_bounded(smem_u32(&t.done), 0);
     }
   } else if (warp < 8) {
@@ -624,7 +646,6 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       const int first = L + ((row0 + 128 * m) >> p.group_shift) + p.self;
       const int last = L + ((row0 + min(rows, 128 * m + 128) - 1) >> p.group_shift) + p.self;
       const int lo_last = p.window ? max(0, last - p.window) : 0;
-      const bool full_tile = rows >= 128 * m + 128;
       const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
       const uint32_t ts = tmem + lanes + 128 * m, to = tmem + lanes + 256 + D * m;
       float ref = -1e30f, sum = 0.f;
@@ -639,11 +660,15 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         for (int i = 0; i < 4; ++i) tmem_ld32(ts + 32 * i, s[i]);
 #pragma unroll
         for (int i = 0; i < 4; ++i) tmem_ld_wait(s[i]);
-        if (!full_tile || p0 + kChunkTokens > first || (p0 < lo_last && p0 + kChunkTokens > p.sinks)) {
-          const int h1 = hi - p0, l1 = lo - p0, s1 = p.sinks - p0;
+        if (p0 + kChunkTokens > first || (p0 < lo_last && p0 + kChunkTokens > p.sinks)) {
+          // one bit per token, so that a token costs a test and a select
 #pragma unroll
-          for (int i = 0; i < 128; ++i)
-            if (i >= h1 || (i < l1 && i >= s1)) s[i >> 5][i & 31] = 0xff800000u;   // -inf
+          for (int i = 0; i < 4; ++i) {
+            const int c = p0 + 32 * i;
+            const uint32_t seen = low_bits(hi - c) & (~low_bits(lo - c) | low_bits(p.sinks - c));
+#pragma unroll
+            for (int e = 0; e < 32; ++e) s[i][e] = (seen >> e) & 1u ? s[i][e] : 0xff800000u;   // -inf
+          }
         }
         float mx[4];
 #pragma unroll
@@ -662,36 +687,42 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
           sum *= a;
           if (j > 0) {   // the product that last added to O has completed: it precedes this S
 #pragma unroll 1
-            for (int i = 0; i < D / 32; ++i) {
-              uint32_t o[32];
-              tmem_ld32(to + 32 * i, o);
+            for (int i = 0; i < D / 16; ++i) {
+              uint32_t o[16];
+              tmem_ld16(to + 16 * i, o);
               tmem_ld_wait(o);
 #pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * a);
-              tmem_st32(to + 32 * i, o);
+              for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * a);
+              tmem_st16(to + 16 * i, o);
             }
           }
         }
         const float2 sc = f2(p.qscale), off = f2(-ref);
         float2 acc[2] = {f2(0.f), f2(0.f)};
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          uint32_t w[32];
+        for (int i = 0; i < 4; ++i) {
+          // in three sweeps, so that 32 exponentials are in flight at a time
+          float2 y[16];
 #pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            const uint32_t* const v = s[2 * i + (e >> 4)] + 2 * (e & 15);
-            const float2 x = __ffma2_rn(make_float2(__uint_as_float(v[0]), __uint_as_float(v[1])), sc, off);
-            const float2 y = make_float2(ex2(x.x), ex2(x.y));
-            acc[e & 1] = __fadd2_rn(acc[e & 1], y);
-            w[e] = narrow2<BF16>(y.x, y.y);
+          for (int e = 0; e < 16; ++e)
+            y[e] = __ffma2_rn(make_float2(__uint_as_float(s[i][2 * e]), __uint_as_float(s[i][2 * e + 1])), sc, off);
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            y[e] = make_float2(ex2(y[e].x), ex2(y[e].y));
           }
-          tmem_st32(ts + 32 * i, w);
+          uint32_t w[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            acc[e & 1] = __fadd2_rn(acc[e & 1], y[e]);
+            w[e] = narrow2<BF16>(y[e].x, y[e].y);
+          }
+          tmem_st16(ts + 16 * i, w);
         }
-        sum += (acc[0].x + acc[0].y) + (acc[1].x + acc[1].y);
         tmem_st_wait();
         tmem_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&t.p_ready[m]));
+        sum += (acc[0].x + acc[0].y) + (acc[1].x + acc[1].y);
       }
       ok = ok && __all_sync(kFull, chunk_wait(&t.done, 0, t, p.status));
       tmem_fence_after();

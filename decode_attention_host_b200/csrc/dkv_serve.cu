@@ -329,7 +329,10 @@ int dkv_attn_chunk(dkv_handle* h, const void* q, int64_t q_stride, const int32_t
   p.sinks = window ? sinks : 0;
   p.self = include_self;
   p.qscale = h->qscale;
-  const long long row_tiles = (static_cast<long long>(total_rows) * h->G) / dkv::kChunkRows + batch;
+  // sum over b of ceil(rows_b G / 256), rows_b unknown here, is at most this
+  const long long row_tiles =
+      (static_cast<long long>(total_rows) * h->G + static_cast<long long>(batch) * (dkv::kChunkRows - h->G)) /
+      dkv::kChunkRows;
   const long long units = row_tiles * c.num_kv_heads;
   long long see = p.max_len;   // tokens that a row tile may walk over
   if (window && static_cast<long long>(window) + sinks + 2 * dkv::kChunkRows < see)
