@@ -122,6 +122,12 @@ def _load() -> ctypes.CDLL:
 
 lib = _load()
 
+try:
+    from . import _dkv_call
+except ImportError as e:
+    raise ImportError("_dkv_call.so is missing: build it with `python decode_attention_host_b200/build.py`") from e
+_dkv_call.load(str(LIB_PATH))
+
 
 def _check(rc: int) -> None:
     if rc != DKV_OK:
@@ -179,33 +185,33 @@ def dkv_attn_decode_multi(h, num_queries, q, k_host, v_host, k_dev, v_dev, block
                                      int(block_table_stride), int(num_dev_blocks)))
 
 
+# The entry points of a serving step go through _dkv_call, which reads the arguments without ctypes: addresses may
+# be tensors, whole numbers or None.
+
 def dkv_extend_tables(h, seq_lens, new_lens, batch, block_table, block_table_stride, free_ids, free_capacity,
                       free_count, free_left, q_start, slot_map, max_slots, stream) -> None:
-    _check(lib.dkv_extend_tables(h, _p(seq_lens), _p(new_lens), int(batch), _p(block_table), int(block_table_stride),
-                                 _p(free_ids), int(free_capacity), _p(free_count), _p(free_left), _p(q_start),
-                                 _p(slot_map), int(max_slots), stream))
+    _check(_dkv_call.extend_tables(h, seq_lens, new_lens, batch, block_table, block_table_stride, free_ids,
+                                   free_capacity, free_count, free_left, q_start, slot_map, max_slots, stream))
 
 
 def dkv_store_kv(h, k_new, v_new, row_stride, slot_map, num_rows, host_split, k_host, v_host, k_dev, v_dev, stream,
                  num_dev_blocks) -> None:
-    _check(lib.dkv_store_kv(h, _p(k_new), _p(v_new), int(row_stride), _p(slot_map), int(num_rows), int(host_split),
-                            _p(k_host), _p(v_host), _p(k_dev), _p(v_dev), stream, int(num_dev_blocks)))
+    _check(_dkv_call.store_kv(h, k_new, v_new, row_stride, slot_map, num_rows, host_split, k_host, v_host, k_dev,
+                              v_dev, stream, num_dev_blocks))
 
 
 def dkv_attn_chunk(h, q, q_stride, q_start, total_rows, k_host, v_host, k_dev, v_dev, block_table, seq_lens,
                    host_split, out, window, sinks, include_self, stream, batch, block_table_stride, num_dev_blocks,
                    k_stage=None, v_stage=None) -> None:
-    _check(lib.dkv_attn_chunk(h, _p(q), int(q_stride), _p(q_start), int(total_rows), _p(k_host), _p(v_host),
-                              _p(k_dev), _p(v_dev), _p(block_table), _p(seq_lens), int(host_split), _p(out),
-                              int(window), int(sinks), int(include_self), stream, int(batch),
-                              int(block_table_stride), int(num_dev_blocks), _p(k_stage), _p(v_stage)))
+    _check(_dkv_call.attn_chunk(h, q, q_stride, q_start, total_rows, k_host, v_host, k_dev, v_dev, block_table,
+                                seq_lens, host_split, out, window, sinks, include_self, stream, batch,
+                                block_table_stride, num_dev_blocks, k_stage, v_stage))
 
 
 def dkv_attn_decode_window(h, window, sinks, include_self, q, k_host, v_host, k_dev, v_dev, block_table, seq_lens,
                            host_split, out, stream, batch, block_table_stride, num_dev_blocks) -> None:
-    _check(lib.dkv_attn_decode_window(h, int(window), int(sinks), int(include_self), _p(q), _p(k_host), _p(v_host),
-                                      _p(k_dev), _p(v_dev), _p(block_table), _p(seq_lens), int(host_split), _p(out),
-                                      stream, int(batch), int(block_table_stride), int(num_dev_blocks)))
+    _check(_dkv_call.attn_decode_window(h, window, sinks, include_self, q, k_host, v_host, k_dev, v_dev, block_table,
+                                        seq_lens, host_split, out, stream, batch, block_table_stride, num_dev_blocks))
 
 
 def dkv_get_status(h: int) -> int:

@@ -9,6 +9,7 @@ from __future__ import annotations
 import os
 import subprocess
 import sys
+import sysconfig
 from pathlib import Path
 
 PKG = Path(__file__).resolve().parent
@@ -19,6 +20,8 @@ SOURCES = [CSRC / "dkv_api.cu", CSRC / "dkv_noalloc.cu", CSRC / "dkv_serve.cu", 
 HEADERS = [CSRC / "dkv_kernels.cuh", CSRC / "dkv_append.cuh", CSRC / "dkv_multi.cuh", CSRC / "dkv_chunk.cuh",
            CSRC / "dkv_tables.cuh", CSRC / "dkv_handle.h", CSRC / "dkv_error.h", CSRC / "dkv_plan.h",
            CSRC / "dkv_tma.h", ROOT / "include" / "dkv.h"]
+CALL_LIB = PKG / "_dkv_call.so"
+CALL_SOURCE = CSRC / "dkv_python.cpp"
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 FLAGS = ["-O3", "-std=c++17", "-gencode", "arch=compute_100a,code=sm_100a", "-lineinfo",
          "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden", "-shared", "-cudart", "static",
@@ -26,10 +29,22 @@ FLAGS = ["-O3", "-std=c++17", "-gencode", "arch=compute_100a,code=sm_100a", "-li
 
 
 def up_to_date() -> bool:
-    if not LIB.exists():
+    if not LIB.exists() or not CALL_LIB.exists():
         return False
-    t = LIB.stat().st_mtime
-    return all(p.stat().st_mtime <= t for p in SOURCES + HEADERS + [Path(__file__)])
+    t = min(LIB.stat().st_mtime, CALL_LIB.stat().st_mtime)
+    return all(p.stat().st_mtime <= t for p in SOURCES + HEADERS + [CALL_SOURCE, Path(__file__)])
+
+
+def build_calls(force: bool = False) -> Path:
+    """Compile the CPython calls (host code only; they open libdkv.so at import)."""
+    newest = max(p.stat().st_mtime for p in (CALL_SOURCE, ROOT / "include" / "dkv.h", Path(__file__)))
+    if force or not CALL_LIB.exists() or CALL_LIB.stat().st_mtime < newest:
+        tmp = CALL_LIB.with_suffix(f".{os.getpid()}.tmp.so")
+        subprocess.run(["g++", "-O2", "-std=c++17", "-Wall", "-fPIC", "-fvisibility=hidden", "-shared",
+                        f"-I{sysconfig.get_paths()['include']}", f"-I{ROOT / 'include'}", "-o", str(tmp),
+                        str(CALL_SOURCE), "-ldl"], check=True)
+        os.replace(tmp, CALL_LIB)
+    return CALL_LIB
 
 
 def build(force: bool = False, verbose: bool = False, out: Path = LIB, defines: tuple[str, ...] = ()) -> Path:
@@ -42,6 +57,7 @@ def build(force: bool = False, verbose: bool = False, out: Path = LIB, defines: 
            *map(str, SOURCES)]
     subprocess.run(cmd, check=True)
     os.replace(tmp, out)
+    build_calls(force)
     return out
 
 

@@ -348,13 +348,13 @@ int dkv_attn_chunk(dkv_handle* h, const void* q, int64_t q_stride, const int32_t
   const long long host_rows = host_split * block_rows, dev_rows = num_dev_blocks * block_rows;
   if (host_rows >= (1LL << 31) || dev_rows >= (1LL << 31))
     return set_error(DKV_ERR_INVALID_ARG, "dkv_attn_chunk: a pool holds 2^31 or more token rows");
-  // a pool that is not there is never copied from: its map is the other's
   p.oob_host = dev_rows == 0;
   p.oob_row = static_cast<int32_t>(dev_rows ? dev_rows : host_rows);
-  if (!dkv::encode_box_map(&maps.k_dev, dev_rows ? k_dev : k_host, dev_rows ? dev_rows : host_rows, c.head_dim, p.box) ||
-      !dkv::encode_box_map(&maps.v_dev, dev_rows ? v_dev : v_host, dev_rows ? dev_rows : host_rows, c.head_dim, p.box) ||
-      !dkv::encode_box_map(&maps.k_host, host_rows ? k_host : k_dev, host_rows ? host_rows : dev_rows, c.head_dim, p.box) ||
-      !dkv::encode_box_map(&maps.v_host, host_rows ? v_host : v_dev, host_rows ? host_rows : dev_rows, c.head_dim, p.box))
+  const int D = c.head_dim;
+  if ((dev_rows && (!dkv::encode_box_map(&maps.k_dev, k_dev, dev_rows, D, p.box) ||
+                    !dkv::encode_box_map(&maps.v_dev, v_dev, dev_rows, D, p.box))) ||
+      (host_rows && (!dkv::encode_box_map(&maps.k_host, k_host, host_rows, D, p.box) ||
+                     !dkv::encode_box_map(&maps.v_host, v_host, host_rows, D, p.box))))
     return set_error(DKV_ERR_CUDA, "cuTensorMapEncodeTiled rejected the pool's tensor map");
   DKV_CUDA(by_shape(c, LaunchChunk{s, p, maps, static_cast<int>(units * p.nsplit)}));
   h->last_launches = p.nsplit > 1 ? 2 : 1;
