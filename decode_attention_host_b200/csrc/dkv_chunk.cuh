@@ -195,12 +195,15 @@ __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.
 
 // ----------------------------------------------------------------------------- small helpers
 
-// cos / sin of position pos for a pair of `turns` per position: the product
+// The angle of position pos for a pair of `turns` per position: the product
 // modulo 2^64 is the angle modulo one turn, its top 32 bits as a signed number
-// the angle in [-1/2, 1/2) turns (off by 2^-24 of a half turn in fp32).
-__device__ __forceinline__ void turn_cs(int pos, uint64_t turns, float& c, float& s) {
+// the angle in [-1/2, 1/2) turns; in radians, off by 2^-24 of its value in fp32.
+__device__ __forceinline__ float turn_angle(int pos, uint64_t turns) {
   const int32_t frac = static_cast<int32_t>((static_cast<uint64_t>(static_cast<uint32_t>(pos)) * turns) >> 32);
-  __sincosf(static_cast<float>(frac) * 1.4629180792671596e-9f, &s, &c);   // 2 pi / 2^32
+  return static_cast<float>(frac) * 1.4629180792671596e-9f;   // 2 pi / 2^32
+}
+__device__ __forceinline__ void turn_cs(int pos, uint64_t turns, float& c, float& s) {
+  __sincosf(turn_angle(pos, turns), &s, &c);
 }
 
 template <bool BF16>
@@ -387,6 +390,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   __syncthreads();
   tmem_fence_after();
   const uint32_t tmem = t.tmem;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the joining kernel waits for the results itself
   // TMEM columns: S (and P over its first half) of row tile i at 128 i, O at 256 + D i
 
   if (warp < 4) {
@@ -522,8 +526,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     if constexpr (ROPE) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        turn_cs(kStep, p.turns[8 * c + 2 * i], E[i].x, F[i].x);
-        turn_cs(kStep, p.turns[8 * c + 2 * i + 1], E[i].y, F[i].y);
+        // to the last bit, as the recurrence repeats their error
+        sincosf(turn_angle(kStep, p.turns[8 * c + 2 * i]), &F[i].x, &E[i].x);
+        sincosf(turn_angle(kStep, p.turns[8 * c + 2 * i + 1]), &F[i].y, &E[i].y);
       }
     }
     int next_pos = -1, chain = 0;
@@ -605,13 +610,13 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         const uint16_t* const qr = p.q + (live ? row : 0) * p.q_stride + static_cast<size_t>(head) * D;
         char* const dst = sq + m * C::kTile + r * 128;
         uint32_t mx = 0;
-#pragma unroll 1
+        uint4 all[D / 8];   // every load in flight at once: the tile cannot begin before the last
+#pragma unroll
+        for (int c = 0; c < D / 8; ++c)
+          all[c] = live ? *reinterpret_cast<const uint4*>(qr + 8 * c) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
         for (int c = 0; c < D / 16; ++c) {
-          uint4 ux = make_uint4(0u, 0u, 0u, 0u), uy = ux;
-          if (live) {
-            ux = *reinterpret_cast<const uint4*>(qr + 8 * c);
-            uy = *reinterpret_cast<const uint4*>(qr + D / 2 + 8 * c);
-          }
+          uint4 ux = all[c], uy = all[c + D / 16];
           if constexpr (ROPE) {
             const uint32_t wx[4] = {ux.x, ux.y, ux.z, ux.w}, wy[4] = {uy.x, uy.y, uy.z, uy.w};
             uint32_t o[8];

@@ -259,7 +259,9 @@ struct RopeTables {
 
 // Fill the tables from the D/2 frequencies (all threads of the block; the
 // caller synchronises).  rope == false stores zero frequencies.
-template <int D>
+// EXACT: the step factors to the last bit of fp32 (__sincosf is off by 2^-21.4,
+// which 64 steps of the recurrence add up to 2e-5 of a pair's norm).
+template <int D, bool EXACT = false>
 __device__ __forceinline__ void rope_fill_tables(RopeTables<D / 16>& t, const double* inv_freq, bool rope,
                                                  int tid, int nthreads) {
   constexpr int PPL = D / 16;
@@ -268,7 +270,14 @@ __device__ __forceinline__ void rope_fill_tables(RopeTables<D / 16>& t, const do
     const int l = i / PPL, r = i % PPL;
     t.freq[r][l] = w;
     float c, sn;
-    rope_cs(4, w, c, sn);
+    if constexpr (EXACT) {
+      double cd, sd;
+      sincos(4.0 * w, &sd, &cd);
+      c = static_cast<float>(cd);
+      sn = static_cast<float>(sd);
+    } else {
+      rope_cs(4, w, c, sn);
+    }
     reinterpret_cast<float*>(&t.e[r >> 1][l])[r & 1] = c;
     reinterpret_cast<float*>(&t.f[r >> 1][l])[r & 1] = sn;
   }
@@ -733,7 +742,7 @@ __global__ void __launch_bounds__(kThreads) split_kernel(const SplitParams p, co
       mbar_init_fence();
     }
   }
-  rope_fill_tables<D>(s_rope, p.inv_freq, ROPE, threadIdx.x, kThreads);
+  rope_fill_tables<D, WIN>(s_rope, p.inv_freq, ROPE, threadIdx.x, kThreads);
   __syncthreads();
 
   // 4-position step factors of this lane's pairs, kept in registers

@@ -5,6 +5,7 @@
 
 #include <climits>
 #include <cstdint>
+#include <string>
 
 #include "dkv.h"
 #include "dkv_chunk.cuh"
@@ -184,7 +185,8 @@ int dkv_extend_tables(dkv_handle* h, const int32_t* seq_lens, const int32_t* new
   if (!seq_lens || !new_lens || !block_table || !free_count || !free_left || !q_start ||
       (!free_ids && free_capacity > 0) || (!slot_map && max_slots > 0))
     return set_error(DKV_ERR_INVALID_ARG, "dkv_extend_tables: null pointer");
-  if (block_table_stride < 1 || free_capacity < 0 || max_slots < 0 || max_slots > (1 << 30))
+  if (block_table_stride < 1 || free_capacity < 0 || free_capacity > (1 << 30) || max_slots < 0 ||
+      max_slots > (1 << 30))
     return set_error(DKV_ERR_INVALID_ARG, "dkv_extend_tables: stride, free_capacity or max_slots out of range");
   if (misaligned(slot_map, 8)) return set_error(DKV_ERR_INVALID_ARG, "dkv_extend_tables: slot_map must be 8-byte aligned");
   dkv::DeviceGuard guard(c.device);
@@ -207,9 +209,11 @@ int dkv_extend_tables(dkv_handle* h, const int32_t* seq_lens, const int32_t* new
   p.free_capacity = free_capacity;
   p.max_slots = max_slots;
   p.div_bs = dkv::make_invdiv(c.block_size);
-  // one CTA while a thread has at most 4 slots, up to one CTA per SM
-  const long long want = (static_cast<long long>(max_slots) + 4 * dkv::kTableThreads - 1) / (4 * dkv::kTableThreads);
-  const int ctas = static_cast<int>(want < 1 ? 1 : want > h->sm_count ? h->sm_count : want);
+  p.wide = !misaligned(slot_map, 16);
+  // a run of slots per thread, up to one wave
+  constexpr long long kRun = dkv::kTableRun * dkv::kTableThreads;
+  const long long want = (static_cast<long long>(max_slots) + kRun - 1) / kRun, wave = dkv::kTableCtasPerSm * h->sm_count;
+  const int ctas = static_cast<int>(want < 1 ? 1 : want > wave ? wave : want);
   dkv::extend_tables_kernel<<<ctas, dkv::kTableThreads, dkv::table_smem_bytes(batch),
                               reinterpret_cast<cudaStream_t>(stream)>>>(p);
   DKV_CUDA(cudaGetLastError());
@@ -351,11 +355,17 @@ int dkv_attn_chunk(dkv_handle* h, const void* q, int64_t q_stride, const int32_t
   p.oob_host = dev_rows == 0;
   p.oob_row = static_cast<int32_t>(dev_rows ? dev_rows : host_rows);
   const int D = c.head_dim;
-  if ((dev_rows && (!dkv::encode_box_map(&maps.k_dev, k_dev, dev_rows, D, p.box) ||
-                    !dkv::encode_box_map(&maps.v_dev, v_dev, dev_rows, D, p.box))) ||
-      (host_rows && (!dkv::encode_box_map(&maps.k_host, k_host, host_rows, D, p.box) ||
-                     !dkv::encode_box_map(&maps.v_host, v_host, host_rows, D, p.box))))
-    return set_error(DKV_ERR_CUDA, "cuTensorMapEncodeTiled rejected the pool's tensor map");
+  int code = 0;
+  if (dev_rows) {
+    code = dkv::encode_box_map(&maps.k_dev, k_dev, dev_rows, D, p.box);
+    if (code == 0) code = dkv::encode_box_map(&maps.v_dev, v_dev, dev_rows, D, p.box);
+  }
+  if (code == 0 && host_rows) {
+    code = dkv::encode_box_map(&maps.k_host, k_host, host_rows, D, p.box);
+    if (code == 0) code = dkv::encode_box_map(&maps.v_host, v_host, host_rows, D, p.box);
+  }
+  if (code != 0)
+    return set_error(DKV_ERR_CUDA, "cuTensorMapEncodeTiled rejected the pool's tensor map (" + std::to_string(code) + ")");
   DKV_CUDA(by_shape(c, LaunchChunk{s, p, maps, static_cast<int>(units * p.nsplit)}));
   h->last_launches = p.nsplit > 1 ? 2 : 1;
   return DKV_OK;
@@ -393,7 +403,9 @@ int dkv_attn_decode_window(dkv_handle* h, int32_t window, int32_t sinks, int32_t
   const long long sb = (static_cast<long long>(sinks) + c.block_size - 1) / c.block_size;
   const int vis = static_cast<int>(wb + sb < nblk ? wb + sb : nblk);
   const long per = static_cast<long>(batch) * c.num_kv_heads;
-  const dkv::SplitPlan pl = dkv::plan_split(vis, per, c.block_size, h->units_target, 0);
+  const dkv::SplitPlan pl =
+      dkv::plan_split_even(vis, per, c.block_size, h->units_target,
+                           static_cast<long>(h->part_rows / (static_cast<size_t>(batch) * c.num_q_heads)));
   if (static_cast<size_t>(batch) * c.num_q_heads * pl.nsplit > h->part_rows)
     return set_error(DKV_ERR_INVALID_ARG, "internal: split plan exceeds the workspace");
   dkv::SplitParams sp{};

@@ -23,7 +23,9 @@
 namespace dkv {
 
 constexpr int kTableThreads = 512;
-constexpr int kTableMaxBatch = 8192;        // both prefix sums fit in 96 KB of shared memory
+constexpr int kTableMaxBatch = 8192;        // both prefix sums and the lengths fit in 96 KB of shared memory
+constexpr int kTableCtasPerSm = 3;
+constexpr int kTableRun = 4;                // consecutive slots a thread maps at a time
 constexpr int kStatusBadId = 1;             // DKV_STATUS_BAD_BLOCK_ID
 constexpr int kStatusBadLen = 2;            // DKV_STATUS_BAD_SEQ_LEN
 constexpr int kStatusNoBlocks = 16;         // DKV_STATUS_NO_FREE_BLOCKS
@@ -41,11 +43,18 @@ struct TableParams {
   int32_t* status;
   int32_t* done;              // CTAs finished; zero between launches
   int32_t batch, stride, block_size, max_len, free_capacity, max_slots;
+  int32_t wide;               // slot_map is 16-byte aligned
   InvDiv div_bs;
 };
 
 __host__ __device__ constexpr size_t table_smem_bytes(int batch) {
-  return 2 * sizeof(int32_t) * (static_cast<size_t>(batch) + 1);
+  return 3 * sizeof(int32_t) * (static_cast<size_t>(batch) + 1);
+}
+
+// Component-wise sum, saturating at 2^30 + 1: more than max_slots or the free list may hold.
+__device__ __forceinline__ uint2 sat_add(uint2 a, uint2 b) {
+  constexpr uint32_t kTop = (1u << 30) + 1;
+  return make_uint2(min(a.x + b.x, kTop), min(a.y + b.y, kTop));
 }
 
 // Largest b with start[b] <= x, for start[0] = 0 <= x < start[n].
@@ -59,104 +68,119 @@ __device__ __forceinline__ int owner_of(const int32_t* start, int n, int x) {
   return lo;
 }
 
-__global__ void __launch_bounds__(kTableThreads) extend_tables_kernel(const TableParams p) {
+__global__ void __launch_bounds__(kTableThreads, kTableCtasPerSm) extend_tables_kernel(const TableParams p) {
   constexpr int NW = kTableThreads / 32;
   extern __shared__ int32_t table_smem[];
   int32_t* const s_start = table_smem;                  // [batch + 1] q_start
   int32_t* const s_first = table_smem + p.batch + 1;    // [batch + 1] first new block
-  __shared__ unsigned long long s_sum[NW][2];
+  int32_t* const s_ctx = s_first + p.batch + 1;         // [batch] tokens before the step
+  __shared__ uint2 s_sum[NW];
   __shared__ int s_bad;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (tid == 0) s_bad = 0;
   const int top = *p.free_count;
   __syncthreads();
 
-  // both prefix sums, kTableThreads sequences at a time, in 64 bits
-  unsigned long long base_t = 0, base_b = 0;
+  // both prefix sums, kTableThreads sequences at a time, in 32 bits that
+  // saturate above every count a call may reach (2^30)
+  uint2 base = make_uint2(0u, 0u);
   for (int b0 = 0; b0 < p.batch; b0 += kTableThreads) {
     const int b = b0 + tid;
-    unsigned long long t = 0, nb = 0;
+    uint2 mine = make_uint2(0u, 0u);
     if (b < p.batch) {
       const long long ctx = p.seq_lens[b], add = p.new_lens[b];
+      s_ctx[b] = static_cast<int32_t>(ctx);
       if (ctx < 0 || add < 0 || ctx + add > p.max_len) {
         s_bad = 1;
       } else {
-        t = static_cast<unsigned long long>(add);
-        nb = static_cast<unsigned long long>(p.div_bs.div(static_cast<int>(ctx + add) + p.block_size - 1) -
-                                             p.div_bs.div(static_cast<int>(ctx) + p.block_size - 1));
+        mine.x = static_cast<uint32_t>(add);
+        mine.y = static_cast<uint32_t>(p.div_bs.div(static_cast<int>(ctx + add) + p.block_size - 1) -
+                                       p.div_bs.div(static_cast<int>(ctx) + p.block_size - 1));
       }
     }
-    unsigned long long it = t, ib = nb;
+    uint2 inc = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const unsigned long long ut = __shfl_up_sync(kFull, it, o), ub = __shfl_up_sync(kFull, ib, o);
-      if (lane >= o) {
-        it += ut;
-        ib += ub;
-      }
+      const uint2 u = make_uint2(__shfl_up_sync(kFull, inc.x, o), __shfl_up_sync(kFull, inc.y, o));
+      if (lane >= o) inc = sat_add(inc, u);
     }
-    if (lane == 31) {
-      s_sum[warp][0] = it;
-      s_sum[warp][1] = ib;
-    }
+    if (lane == 31) s_sum[warp] = inc;
     __syncthreads();
-    unsigned long long ot = base_t, ob = base_b, at = 0, ab = 0;
+    uint2 before = base, all = make_uint2(0u, 0u);
 #pragma unroll
     for (int w = 0; w < NW; ++w) {
-      if (w < warp) {
-        ot += s_sum[w][0];
-        ob += s_sum[w][1];
-      }
-      at += s_sum[w][0];
-      ab += s_sum[w][1];
+      const uint2 u = s_sum[w];
+      if (w < warp) before = sat_add(before, u);
+      all = sat_add(all, u);
     }
-    // sums past 2^31 are refused below; the stored values are then unused
+    // sums that saturate are refused below; the stored values are then unused
     if (b < p.batch) {
-      s_start[b] = static_cast<int32_t>(ot + it - t);
-      s_first[b] = static_cast<int32_t>(ob + ib - nb);
+      s_start[b] = static_cast<int32_t>(before.x + inc.x - mine.x);
+      s_first[b] = static_cast<int32_t>(before.y + inc.y - mine.y);
     }
-    base_t += at;
-    base_b += ab;
+    base = sat_add(base, all);
     __syncthreads();
   }
   if (tid == 0) {
-    s_start[p.batch] = static_cast<int32_t>(base_t);
-    s_first[p.batch] = static_cast<int32_t>(base_b);
+    s_start[p.batch] = static_cast<int32_t>(base.x);
+    s_first[p.batch] = static_cast<int32_t>(base.y);
   }
   __syncthreads();
   // all or nothing: a call that cannot be served in full changes no table
   // entry, takes no block and maps no slot
   int why = 0;
   if (s_bad) why |= kStatusBadLen;
-  if (base_t > static_cast<unsigned long long>(p.max_slots)) why |= kStatusNoSlots;
-  if (top < 0 || top > p.free_capacity || base_b > static_cast<unsigned long long>(top)) why |= kStatusNoBlocks;
-  const int n_new = why ? 0 : static_cast<int>(base_t);
-  const int n_blk = why ? 0 : static_cast<int>(base_b);
+  if (base.x > static_cast<uint32_t>(p.max_slots)) why |= kStatusNoSlots;
+  if (top < 0 || top > p.free_capacity || base.y > static_cast<uint32_t>(top)) why |= kStatusNoBlocks;
+  const int n_new = why ? 0 : static_cast<int>(base.x);
+  const int n_blk = why ? 0 : static_cast<int>(base.y);
 
   const int gid = blockIdx.x * kTableThreads + tid;
   const int gsz = gridDim.x * kTableThreads;
   for (int k = gid; k < n_blk; k += gsz) {
     const int b = owner_of(s_first, p.batch, k);
-    const int held = p.div_bs.div(p.seq_lens[b] + p.block_size - 1);
+    const int held = p.div_bs.div(s_ctx[b] + p.block_size - 1);
     p.table[static_cast<size_t>(b) * p.stride + held + (k - s_first[b])] = p.free_ids[top - 1 - k];
   }
   int bad_id = 0;
-  for (int i = gid; i < p.max_slots; i += gsz) {
-    int64_t slot = -1;
-    if (i < n_new) {
-      const int b = owner_of(s_start, p.batch, i);
-      const int ctx = p.seq_lens[b];
-      const int pos = ctx + (i - s_start[b]);
-      const int blk = p.div_bs.div(pos);
-      const int held = p.div_bs.div(ctx + p.block_size - 1);
-      // entries below `held` were there before the call; the others are being
-      // written by this launch and are taken from the free list instead
-      const int id = blk < held ? p.table[static_cast<size_t>(b) * p.stride + blk]
-                                : p.free_ids[top - 1 - (s_first[b] + blk - held)];
-      if (id >= 0) slot = static_cast<int64_t>(id) * p.block_size + (pos - blk * p.block_size);
-      else bad_id = kStatusBadId;
+  // Runs of kTableRun slots: one search for the first, the next ones move to the
+  // next sequence or block when they leave theirs (a million slots took 15 us
+  // with a search and two dependent loads for each).
+  for (int i0 = gid * kTableRun; i0 < p.max_slots; i0 += gsz * kTableRun) {
+    int64_t slot[kTableRun];
+    int b = i0 < n_new ? owner_of(s_start, p.batch, i0) : p.batch;
+    int blk = -1, id = -1;
+#pragma unroll
+    for (int r = 0; r < kTableRun; ++r) {
+      const int i = i0 + r;
+      slot[r] = -1;
+      if (i >= n_new) continue;
+      while (s_start[b + 1] <= i) {   // past the end of b, and over sequences without new tokens
+        ++b;
+        blk = -1;
+      }
+      const int pos = s_ctx[b] + (i - s_start[b]);
+      const int at = p.div_bs.div(pos);
+      if (at != blk) {
+        blk = at;
+        const int held = p.div_bs.div(s_ctx[b] + p.block_size - 1);
+        // entries below `held` were there before the call; the others are being
+        // written by this launch and are taken from the free list instead
+        id = blk < held ? p.table[static_cast<size_t>(b) * p.stride + blk]
+                        : p.free_ids[top - 1 - (s_first[b] + blk - held)];
+        if (id < 0) bad_id = kStatusBadId;
+      }
+      if (id >= 0) slot[r] = static_cast<int64_t>(id) * p.block_size + (pos - blk * p.block_size);
     }
-    p.slot_map[i] = slot;
+    if (p.wide && i0 + kTableRun <= p.max_slots) {
+      longlong2* const o = reinterpret_cast<longlong2*>(p.slot_map + i0);
+      o[0] = make_longlong2(slot[0], slot[1]);
+      o[1] = make_longlong2(slot[2], slot[3]);
+    } else {
+#pragma unroll
+      for (int r = 0; r < kTableRun; ++r)
+        if (i0 + r < p.max_slots) p.slot_map[i0 + r] = slot[r];
+    }
   }
   for (int b = gid; b <= p.batch; b += gsz) p.q_start[b] = why ? 0 : s_start[b];
   if (bad_id) atomicOr(p.status, bad_id);

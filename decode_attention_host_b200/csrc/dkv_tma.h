@@ -35,29 +35,30 @@ inline PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
 // of D 16-bit elements starting at `pool` (16-byte aligned): boxes of 16 rows,
 // either whole plain rows (`plain`, the K pool) or 64-element halves with the
 // 128-byte swizzle (the V pool).  A null pool or zero rows gives a zeroed map
-// that no copy uses.  Returns false if the driver rejects the map.
-inline bool encode_map(CUtensorMap* map, const void* pool, long long rows, int D, int box_cols, int box_rows,
-                       bool swizzle) {
+// that no copy uses.
+// Returns the driver's error code (0: none), or -1 if it has no encoder.
+inline int encode_map(CUtensorMap* map, const void* pool, long long rows, int D, int box_cols, int box_rows,
+                      bool swizzle) {
   *map = CUtensorMap{};
-  if (!pool || rows <= 0) return true;
+  if (!pool || rows <= 0) return 0;
   PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
-  if (!enc) return false;
+  if (!enc) return -1;
   const cuuint64_t dims[2] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(rows)};
   const cuuint64_t strides[1] = {static_cast<cuuint64_t>(D) * 2};
   const cuuint32_t box[2] = {static_cast<cuuint32_t>(box_cols), static_cast<cuuint32_t>(box_rows)};
   const cuuint32_t estride[2] = {1, 1};
-  return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, const_cast<void*>(pool), dims, strides, box, estride,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
-             CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  return static_cast<int>(enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, const_cast<void*>(pool), dims, strides, box,
+                              estride, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                              swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+                              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE));
 }
 inline bool encode_pool_map(CUtensorMap* map, const void* pool, long long rows, int D, bool plain) {
-  return encode_map(map, pool, rows, D, plain ? D : 64, kTileTokens, !plain);
+  return encode_map(map, pool, rows, D, plain ? D : 64, kTileTokens, !plain) == 0;
 }
 
 // The same pool in swizzled boxes of `box_rows` (up to 256) rows x 64 elements; rows
 // outside it fill with zeros.
-inline bool encode_box_map(CUtensorMap* map, const void* pool, long long rows, int D, int box_rows) {
+inline int encode_box_map(CUtensorMap* map, const void* pool, long long rows, int D, int box_rows) {
   return encode_map(map, pool, rows, D, 64, box_rows, true);
 }
 

@@ -219,7 +219,7 @@ DKV_API int dkv_append_kv(dkv_handle* h, const float* x, const void* w_k, const 
  *                 min(block_table_stride, max_blocks_per_seq) * S
  *   block_table   device int32 [batch][block_table_stride]: entries of new
  *                 blocks are written, all others left as they are
- *   free_ids      device int32 [free_capacity]; free_count device int32 [1]:
+ *   free_ids      device int32 [free_capacity], at most 2^30; free_count device int32 [1]:
  *                 the stack's entries are free_ids[0 .. free_count), the k-th
  *                 block taken is free_ids[free_count - 1 - k]
  *   free_left     device int32 [1], written: free_count less the blocks taken;
