@@ -35,6 +35,8 @@
 // poisons the rows that see it and sets a status bit.
 #pragma once
 
+#include <type_traits>
+
 #include "dkv_kernels.cuh"
 
 namespace dkv {
@@ -95,6 +97,7 @@ struct ChunkTail {
   uint64_t done;                               // every product has completed
   uint32_t tmem;
   int32_t b, tile;                             // the CTA's sequence (-1: none) and row tile
+  int32_t q0, n, len;                          // its first row, rows and cached tokens
   int32_t poison;                              // an invalid block id or an operand out of range
   int32_t broken;                              // a wait ran out: every role gives up
 };
@@ -287,11 +290,15 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   const int slot = p.div_hkv.div(unit);
   const int h = unit - slot * p.hkv;
   if (warp == 0) {
-    int before = 0, fb = -1, ft = 0;
+    // 32 sequences at a time, each lane with its rows and length in hand
+    int before = 0, fb = -1, ft = 0, fq = 0, fn = 0, fl = 0;
     for (int b0 = p.batch - 1; b0 >= 0 && fb < 0; b0 -= 32) {
       const int b = b0 - lane;
-      const int n = b >= 0 ? p.q_start[b + 1] - p.q_start[b] : 0;
-      const int tiles = n > 0 ? static_cast<int>(((static_cast<long long>(n) << p.group_shift) + kChunkRows - 1) / kChunkRows) : 0;
+      const int q = b >= 0 ? p.q_start[b] : 0;
+      const int n = b >= 0 ? p.q_start[b + 1] - q : 0;
+      const int len = b >= 0 ? p.seq_lens[b] : 0;
+      const int tiles =
+          n > 0 ? static_cast<int>(((static_cast<long long>(n) << p.group_shift) + kChunkRows - 1) / kChunkRows) : 0;
       int inc = tiles;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -303,22 +310,42 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         const int src = __ffs(hit) - 1;
         fb = b0 - src;
         ft = __shfl_sync(kFull, before + inc - 1 - slot, src);
+        fq = __shfl_sync(kFull, q, src);
+        fn = __shfl_sync(kFull, n, src);
+        fl = __shfl_sync(kFull, len, src);
       }
       before += __shfl_sync(kFull, inc, 31);
     }
     if (lane == 0) {
       t.b = fb;
       t.tile = ft;
+      t.q0 = fq;
+      t.n = fn;
+      t.len = fl;
       t.poison = 0;
       t.broken = 0;
     }
+  } else if (warp == 1 && lane == 0) {
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(smem_u32(&t.k_full[i]), 1);
+      mbar_init(smem_u32(&t.k_ready[i]), 4);
+      mbar_init(smem_u32(&t.k_free[i]), 1);
+      mbar_init(smem_u32(&t.v_full[i]), 1);
+      mbar_init(smem_u32(&t.v_free[i]), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&t.q_ready[i]), 4);
+      mbar_init(smem_u32(&t.s_full[i]), 1);
+      mbar_init(smem_u32(&t.p_ready[i]), 4);
+    }
+    mbar_init(smem_u32(&t.done), 1);
+    mbar_init_fence();
+    t.tmem = 0;
   }
   __syncthreads();
   const int b = t.b;
   if (b < 0) return;
-  const int q0 = p.q_start[b];
-  const int n = p.q_start[b + 1] - q0;
-  const int L = p.seq_lens[b];
+  const int q0 = t.q0, n = t.n, L = t.len;
   const int row0 = t.tile * kChunkRows;
   const int rows = min((n << p.group_shift) - row0, kChunkRows);
   const int num_m = rows > 128 ? 2 : 1;
@@ -345,53 +372,30 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   const long long row = static_cast<long long>(q0) + tok;
   const bool live = m >= 0 && tok < n && row >= 0 && row < p.total_rows;
 
+  // this thread's row with one value: zero (an empty split), or NaN
+  auto one_value = [&](bool nan) {
+    if (!live) return;
+    const size_t at = static_cast<size_t>(row) * p.hq + head;
+    if (p.nsplit == 1) {
+      const uint32_t f = nan ? 0x7fff7fffu : 0u;
+      for (int c = 0; c < D / 8; ++c) reinterpret_cast<uint4*>(p.out + at * D)[c] = make_uint4(f, f, f, f);
+    } else {
+      const float f = nan ? __int_as_float(0x7fc00000) : 0.f;
+      float4* o = reinterpret_cast<float4*>(p.part_o + (at * p.nsplit + split) * D);
+      for (int c = 0; c < D / 4; ++c) o[c] = make_float4(f, f, f, f);
+      p.part_lse[at * p.nsplit + split] = nan ? f : -INFINITY;
+    }
+  };
   if (nt == 0 || p.id_total == 0) {
     // no token to see: zero rows; an invalid length, or no pool to look in: NaN rows
     const bool nan = bad_len || (p.id_total == 0 && total > 0);
     if (nan && tid == 0) atomicOr(p.status, bad_len ? 2 : 1);
-    if (live) {
-      const size_t at = static_cast<size_t>(row) * p.hq + head;
-      if (p.nsplit == 1) {
-        const uint32_t f = nan ? 0x7fff7fffu : 0u;
-        for (int c = 0; c < D / 8; ++c) reinterpret_cast<uint4*>(p.out + at * D)[c] = make_uint4(f, f, f, f);
-      } else {
-        const float f = nan ? __int_as_float(0x7fc00000) : 0.f;
-        float4* o = reinterpret_cast<float4*>(p.part_o + (at * p.nsplit + split) * D);
-        for (int c = 0; c < D / 4; ++c) o[c] = make_float4(f, f, f, f);
-        p.part_lse[at * p.nsplit + split] = nan ? f : -INFINITY;
-      }
-    }
+    one_value(nan);
     return;
   }
-
-  if (warp == 1) {
-    if (lane == 0) {
-      for (int i = 0; i < 4; ++i) {
-        mbar_init(smem_u32(&t.k_full[i]), 1);
-        mbar_init(smem_u32(&t.k_ready[i]), 4);
-        mbar_init(smem_u32(&t.k_free[i]), 1);
-        mbar_init(smem_u32(&t.v_full[i]), 1);
-        mbar_init(smem_u32(&t.v_free[i]), 1);
-      }
-      for (int i = 0; i < 2; ++i) {
-        mbar_init(smem_u32(&t.q_ready[i]), 4);
-        mbar_init(smem_u32(&t.s_full[i]), 1);
-        mbar_init(smem_u32(&t.p_ready[i]), 4);
-      }
-      mbar_init(smem_u32(&t.done), 1);
-      mbar_init_fence();
-    }
-    __syncwarp();
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&t.tmem))
-                 : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
-  }
-  tmem_fence_before();
-  __syncthreads();
-  tmem_fence_after();
-  const uint32_t tmem = t.tmem;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the joining kernel waits for the results itself
-  // TMEM columns: S (and P over its first half) of row tile i at 128 i, O at 256 + D i
+  // TMEM columns: S (and P over its first half) of row tile i at 128 i, O at 256 + D i.
+  // The issuing warp allocates them; the others learn the address with their first S.
 
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
@@ -455,11 +459,15 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       }
     } else if (warp == 1) {
       // ------------------------------------------------------------ matrix products
+      asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&t.tmem))
+                   : "memory");
+      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+      __syncwarp();
       constexpr uint32_t kIdQK = umma_idesc(128, kChunkTokens, kOpBf16, false);
       constexpr uint32_t kIdPV = umma_idesc(128, D, BF16, true);
       const uint32_t on = lane == 0;
       const int tiles = __shfl_sync(kFull, nt, 0), row_tiles = __shfl_sync(kFull, num_m, 0);
-      const uint32_t tm = __shfl_sync(kFull, tmem, 0);
+      const uint32_t tm = __shfl_sync(kFull, *reinterpret_cast<volatile uint32_t*>(&t.tmem), 0);
       const uint32_t q_low = desc_low(smem_u32(sq), 16), k_low = desc_low(smem_u32(sk), 16);
       const uint32_t v_low = desc_low(smem_u32(sv), kSubTile);
       auto qk = [&](int mt, int stage) {   // S = Q K^T, both K-major
@@ -604,38 +612,62 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     // -------------------------------------------------------------- softmax, a thread per row
     const int r = tid & 127;
     if (m < num_m) {
-      // the row's query: rotated, to its place in the swizzled tile; rows past the end are zero
+      // The warp's 32 queries: rotated, to their place in the swizzled tile; rows
+      // past the end are zero.  A lane takes 8 pairs of every kPer-th row (one
+      // 16-byte chunk of each half), so that a load covers whole lines, and its
+      // cos / sin advance from row to row as those of the keys do.
       const int pos = L + tok;
       {
-        const uint16_t* const qr = p.q + (live ? row : 0) * p.q_stride + static_cast<size_t>(head) * D;
-        char* const dst = sq + m * C::kTile + r * 128;
+        constexpr int kC = D / 16, kPer = 32 / kC;
+        const int c = lane % kC, r0 = 32 * (warp & 3) + lane / kC;
+        const int first_row = row0 + 128 * m + r0;
+        const int step = kPer >> p.group_shift;
+        uint4 ux[kC], uy[kC];   // every load in flight at once: the first product waits for the last
+#pragma unroll
+        for (int i = 0; i < kC; ++i) {
+          const int id = first_row + kPer * i, tk = id >> p.group_shift;
+          const long long rw = static_cast<long long>(q0) + tk;
+          ux[i] = uy[i] = make_uint4(0u, 0u, 0u, 0u);
+          if (tk < n && rw >= 0 && rw < p.total_rows) {
+            const uint16_t* const src = p.q + rw * p.q_stride +
+                                        static_cast<size_t>((h << p.group_shift) + (id & ((1 << p.group_shift) - 1))) * D + 8 * c;
+            ux[i] = *reinterpret_cast<const uint4*>(src);
+            uy[i] = *reinterpret_cast<const uint4*>(src + D / 2);
+          }
+        }
+        float2 E[4], F[4], Cc[4], Sc[4];
+        if constexpr (ROPE) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint64_t t0 = p.turns[8 * c + 2 * i], t1 = p.turns[8 * c + 2 * i + 1];
+            turn_cs(L + (first_row >> p.group_shift), t0, Cc[i].x, Sc[i].x);
+            turn_cs(L + (first_row >> p.group_shift), t1, Cc[i].y, Sc[i].y);
+            turn_cs(step, t0, E[i].x, F[i].x);
+            turn_cs(step, t1, E[i].y, F[i].y);
+          }
+        }
         uint32_t mx = 0;
-        uint4 all[D / 8];   // every load in flight at once: the tile cannot begin before the last
+        char* const dst = sq + m * C::kTile;
 #pragma unroll
-        for (int c = 0; c < D / 8; ++c)
-          all[c] = live ? *reinterpret_cast<const uint4*>(qr + 8 * c) : make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-        for (int c = 0; c < D / 16; ++c) {
-          uint4 ux = all[c], uy = all[c + D / 16];
+        for (int i = 0; i < kC; ++i) {
+          const int r = r0 + kPer * i;
           if constexpr (ROPE) {
-            const uint32_t wx[4] = {ux.x, ux.y, ux.z, ux.w}, wy[4] = {uy.x, uy.y, uy.z, uy.w};
+            float2 X[4] = {widen2<BF16>(ux[i].x), widen2<BF16>(ux[i].y), widen2<BF16>(ux[i].z), widen2<BF16>(ux[i].w)};
+            float2 Y[4] = {widen2<BF16>(uy[i].x), widen2<BF16>(uy[i].y), widen2<BF16>(uy[i].z), widen2<BF16>(uy[i].w)};
+            rope_rotate_advance<4>(X, Y, Cc, Sc, E, F);
             uint32_t o[8];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              const float2 x = widen2<BF16>(wx[e]), y = widen2<BF16>(wy[e]);
-              float c0, s0, c1, s1;
-              turn_cs(pos, p.turns[8 * c + 2 * e], c0, s0);
-              turn_cs(pos, p.turns[8 * c + 2 * e + 1], c1, s1);
-              o[e] = narrow2<false>(x.x * c0 - y.x * s0, x.y * c1 - y.y * s1);
-              o[4 + e] = narrow2<false>(y.x * c0 + x.x * s0, y.y * c1 + x.y * s1);
+              o[e] = narrow2<false>(X[e].x, X[e].y);
+              o[4 + e] = narrow2<false>(Y[e].x, Y[e].y);
               mx = hmax_abs2(hmax_abs2(mx, o[e]), o[4 + e]);
             }
-            ux = make_uint4(o[0], o[1], o[2], o[3]);
-            uy = make_uint4(o[4], o[5], o[6], o[7]);
+            ux[i] = make_uint4(o[0], o[1], o[2], o[3]);
+            uy[i] = make_uint4(o[4], o[5], o[6], o[7]);
           }
-          *reinterpret_cast<uint4*>(dst + ((c ^ (r & 7)) << 4)) = ux;
-          if constexpr (D == 128) *reinterpret_cast<uint4*>(dst + kSubTile + ((c ^ (r & 7)) << 4)) = uy;
-          else *reinterpret_cast<uint4*>(dst + (((c + 4) ^ (r & 7)) << 4)) = uy;
+          *reinterpret_cast<uint4*>(dst + r * 128 + ((c ^ (r & 7)) << 4)) = ux[i];
+          if constexpr (D == 128) *reinterpret_cast<uint4*>(dst + kSubTile + r * 128 + ((c ^ (r & 7)) << 4)) = uy[i];
+          else *reinterpret_cast<uint4*>(dst + r * 128 + (((c + 4) ^ (r & 7)) << 4)) = uy[i];
         }
         if (has_inf2(mx)) {
           *reinterpret_cast<volatile int32_t*>(&t.poison) = 1;
@@ -652,7 +684,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       const int last = L + ((row0 + min(rows, 128 * m + 128) - 1) >> p.group_shift) + p.self;
       const int lo_last = p.window ? max(0, last - p.window) : 0;
       const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-      const uint32_t ts = tmem + lanes + 128 * m, to = tmem + lanes + 256 + D * m;
+      uint32_t ts = 0, to = 0;
       float ref = -1e30f, sum = 0.f;
       bool ok = true;
       for (int j = 0; j < nt; ++j) {
@@ -660,6 +692,11 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         ok = __all_sync(kFull, chunk_wait(&t.s_full[m], j & 1, t, p.status));
         if (!ok) break;
         tmem_fence_after();
+        if (j == 0) {
+          const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(&t.tmem);
+          ts = tmem + lanes + 128 * m;
+          to = tmem + lanes + 256 + D * m;
+        }
         uint32_t s[4][32];
 #pragma unroll
         for (int i = 0; i < 4; ++i) tmem_ld32(ts + 32 * i, s[i]);
@@ -734,32 +771,57 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       // ---- the row's result
       const bool nan = !ok || *reinterpret_cast<volatile int32_t*>(&t.poison);
       const float inv = nan ? __int_as_float(0x7fc00000) : (sum == 0.f ? 0.f : 1.f / sum);
-      const size_t at = static_cast<size_t>(live ? row : 0) * p.hq + head;
-#pragma unroll 1
-      for (int i = 0; i < D / 32; ++i) {
-        uint32_t o[32];
-        tmem_ld32(to + 32 * i, o);
-        tmem_ld_wait(o);
-        if (live && p.nsplit == 1) {
-          uint4* const dst = reinterpret_cast<uint4*>(p.out + at * D + 32 * i);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            uint32_t w[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              w[k] = narrow2<BF16>(__uint_as_float(o[8 * e + 2 * k]) * inv, __uint_as_float(o[8 * e + 2 * k + 1]) * inv);
-            dst[e] = make_uint4(w[0], w[1], w[2], w[3]);
-          }
-        } else if (live) {
-          float4* const dst = reinterpret_cast<float4*>(p.part_o + (at * p.nsplit + split) * D + 32 * i);
-#pragma unroll
-          for (int e = 0; e < 8; ++e)
-            dst[e] = make_float4(__uint_as_float(o[4 * e]) * inv, __uint_as_float(o[4 * e + 1]) * inv,
-                                 __uint_as_float(o[4 * e + 2]) * inv, __uint_as_float(o[4 * e + 3]) * inv);
-        }
+      // A thread's row goes through the block's shared memory, which nothing reads
+      // any more, so that the warp writes whole lines: row by row from the
+      // threads themselves, a CTA's 256 rows of fp32 took 10,600 cycles.
+      char* const buf = chunk_smem + (warp - 8) * (32 * D * 4);
+      auto flush = [&](auto bytes, auto&& place) {   // the warp's 32 rows of `bytes` bytes to place(row of the warp)
+        constexpr int kRow = decltype(bytes)::value, kC = kRow / 16, kPer = 32 / kC;
         __syncwarp();
+#pragma unroll
+        for (int i = 0; i < kC; ++i) {
+          const int r = kPer * i + lane / kC, c = lane % kC;
+          const int id = row0 + 128 * m + 32 * (warp & 3) + r, tk = id >> p.group_shift;
+          const long long rw = static_cast<long long>(q0) + tk;
+          if (tk < n && rw >= 0 && rw < p.total_rows) {
+            const size_t at = static_cast<size_t>(rw) * p.hq + (h << p.group_shift) + (id & ((1 << p.group_shift) - 1));
+            reinterpret_cast<uint4*>(place(at))[c] =
+                *reinterpret_cast<const uint4*>(buf + r * kRow + ((c ^ (r & 7)) << 4));
+          }
+        }
+      };
+      if (ok) {
+#pragma unroll 1
+        for (int i = 0; i < D / 32; ++i) {
+          uint32_t o[32];
+          tmem_ld32(to + 32 * i, o);
+          tmem_ld_wait(o);
+          if (p.nsplit == 1) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              uint32_t w[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                w[k] = narrow2<BF16>(__uint_as_float(o[8 * e + 2 * k]) * inv, __uint_as_float(o[8 * e + 2 * k + 1]) * inv);
+              *reinterpret_cast<uint4*>(buf + lane * (D * 2) + (((4 * i + e) ^ (lane & 7)) << 4)) =
+                  make_uint4(w[0], w[1], w[2], w[3]);
+            }
+          } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              *reinterpret_cast<float4*>(buf + lane * (D * 4) + (((8 * i + e) ^ (lane & 7)) << 4)) =
+                  make_float4(__uint_as_float(o[4 * e]) * inv, __uint_as_float(o[4 * e + 1]) * inv,
+                              __uint_as_float(o[4 * e + 2]) * inv, __uint_as_float(o[4 * e + 3]) * inv);
+          }
+        }
+      } else {   // a wait ran out: copies may still be landing in shared memory
+        one_value(true);
       }
-      if (live && p.nsplit > 1)
+      if (ok && p.nsplit == 1) flush(std::integral_constant<int, D * 2>{}, [&](size_t at) { return p.out + at * D; });
+      if (ok && p.nsplit > 1)
+        flush(std::integral_constant<int, D * 4>{}, [&](size_t at) { return p.part_o + (at * p.nsplit + split) * D; });
+      const size_t at = static_cast<size_t>(live ? row : 0) * p.hq + head;
+      if (ok && live && p.nsplit > 1)
         p.part_lse[at * p.nsplit + split] = nan ? __int_as_float(0x7fc00000) : (sum == 0.f ? -INFINITY : ref + __log2f(sum));
     }
   }
@@ -767,6 +829,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   __syncthreads();
   if (warp == 1) {
     tmem_fence_after();
+    const uint32_t tmem = __shfl_sync(kFull, *reinterpret_cast<volatile uint32_t*>(&t.tmem), 0);
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
   }
 }
