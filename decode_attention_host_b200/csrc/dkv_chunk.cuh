@@ -15,7 +15,7 @@
 // the walk is cut into splits whose partial results a second kernel joins.
 //
 // One CTA per SM, 16 warps:
-//   warp 0      copies K and V tiles, one tensor copy per run of rows that lies
+//   warps 0, 2  copy K and V tiles, one tensor copy per run of rows that lies
 //               in one block (16 to 128 rows) and 64-element half
 //   warp 1      issues the matrix instructions: S = Q K^T into TMEM, then
 //               O += P V with P read from TMEM; the two row tiles alternate, so
@@ -369,13 +369,15 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   const int idx = row0 + (tid & 255);            // threads 256..511 own rows 0..255
   const int tok = idx >> p.group_shift;
   const int head = (h << p.group_shift) + (idx & ((1 << p.group_shift) - 1));
-  const long long row = static_cast<long long>(q0) + tok;
-  const bool live = m >= 0 && tok < n && row >= 0 && row < p.total_rows;
+  // tokens whose rows exist: all n, unless q_start names rows outside the buffers
+  const int n_rows = q0 < 0 || q0 > p.total_rows ? 0 : min(n, p.total_rows - q0);
+  const bool live = m >= 0 && tok < n_rows;
+  auto place_of_row = [&] { return (static_cast<size_t>(live ? q0 + tok : 0)) * p.hq + head; };   // among all rows' heads
 
   // this thread's row with one value: zero (an empty split), or NaN
   auto one_value = [&](bool nan) {
     if (!live) return;
-    const size_t at = static_cast<size_t>(row) * p.hq + head;
+    const size_t at = place_of_row();
     if (p.nsplit == 1) {
       const uint32_t f = nan ? 0x7fff7fffu : 0u;
       for (int c = 0; c < D / 8; ++c) reinterpret_cast<uint4*>(p.out + at * D)[c] = make_uint4(f, f, f, f);
@@ -399,63 +401,70 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
 
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
-    if (warp == 0) {
+    if (warp == 0 || warp == 2) {
       // ------------------------------------------------------------ copies
-      Ring rk, rv;
+      // A warp each for K and V, so that neither waits for the other's stages (K
+      // runs ahead, as it is rotated before its product: with one warp for both
+      // the rotated key tile came last and set the pace, 4280 cycles a tile).
+      // The block ids of the next tile are read while this one's stage is waited for.
+      const bool is_v = warp == 2;
+      const int stages = is_v ? C::kStagesV : C::kStagesK;
+      uint64_t* const full = is_v ? t.v_full : t.k_full;
+      uint64_t* const free_ = is_v ? t.v_free : t.k_free;
+      char* const tiles = is_v ? sv : sk;
+      const CUtensorMap* const dev_map = is_v ? &maps.v_dev : &maps.k_dev;
+      const CUtensorMap* const host_map = is_v ? &maps.v_host : &maps.k_host;
       const int nbox = kChunkTokens / p.box;
       const uint32_t box_bytes = static_cast<uint32_t>(p.box) * 128;
       const int32_t* trow = p.table + static_cast<size_t>(b) * p.stride;
+      auto read_id = [&](int j) {   // of the run of rows that this lane copies; -2: nothing there to see
+        if (lane >= nbox || j >= nt) return -2;
+        const int t0 = tile_pos(j) + lane * p.box;
+        return t0 < hi_max && (t0 + p.box > lo_min || t0 < sk_end) ? max(trow[p.div_bs.div(t0)], -1) : -2;
+      };
+      int stage = 0;
+      uint32_t parity = 0;
+      int next_id = read_id(0);
       for (int j = 0; j < nt; ++j) {
-        // the run of rows this lane copies: block, pool and row, or a row that fills with zeros
+        const int id = next_id;
+        next_id = read_id(j + 1);
+        // the rows to copy: in this pool, or outside it, which fills with zeros
         int y = p.oob_row;
         bool host = p.oob_host != 0;
-        if (lane < nbox) {
+        if (id >= 0 && id < p.id_total) {
           const int t0 = tile_pos(j) + lane * p.box;
-          if (t0 < hi_max && (t0 + p.box > lo_min || t0 < sk_end)) {
-            const int blk = p.div_bs.div(t0);
-            const int id = trow[blk];
-            if (id >= 0 && id < p.id_total) {
-              host = id < p.host_split;
-              y = ((host ? id : id - p.host_split) * p.hkv + h) * p.block_size + (t0 - blk * p.block_size);
-            } else {
-              *reinterpret_cast<volatile int32_t*>(&t.poison) = 1;
-              atomicOr(p.status, 1);
-            }
-          }
+          host = id < p.host_split;
+          y = ((host ? id : id - p.host_split) * p.hkv + h) * p.block_size + (t0 - p.div_bs.div(t0) * p.block_size);
+        } else if (id != -2) {
+          *reinterpret_cast<volatile int32_t*>(&t.poison) = 1;
+          atomicOr(p.status, 1);
         }
         __syncwarp();
-        if (!__all_sync(kFull, chunk_wait(&t.k_free[rk.stage], rk.parity ^ 1u, t, p.status))) break;
-        const uint32_t kb = smem_u32(&t.k_full[rk.stage]);
-        if (lane == 0) mbar_arrive_expect_tx(kb, C::kTile);
+        if (!__all_sync(kFull, chunk_wait(&free_[stage], parity ^ 1u, t, p.status))) break;
+        const uint32_t bar = smem_u32(&full[stage]);
+        if (lane == 0) mbar_arrive_expect_tx(bar, C::kTile);
         __syncwarp();
         if (lane < nbox) {
-          const uint32_t dst = smem_u32(sk + rk.stage * C::kTile) + lane * box_bytes;
+          const uint32_t dst = smem_u32(tiles + stage * C::kTile) + lane * box_bytes;
 #pragma unroll
-          for (int x = 0; x < C::kSub; ++x)
-            tma_load_2d(dst + x * kSubTile, host ? &maps.k_host : &maps.k_dev, 64 * x, y, kb);
+          for (int x = 0; x < C::kSub; ++x) tma_load_2d(dst + x * kSubTile, host ? host_map : dev_map, 64 * x, y, bar);
         }
-        rk.next<C::kStagesK>();
-        if (!__all_sync(kFull, chunk_wait(&t.v_free[rv.stage], rv.parity ^ 1u, t, p.status))) break;
-        const uint32_t vb = smem_u32(&t.v_full[rv.stage]);
-        if (lane == 0) mbar_arrive_expect_tx(vb, C::kTile);
-        __syncwarp();
-        if (lane < nbox) {
-          const uint32_t dst = smem_u32(sv + rv.stage * C::kTile) + lane * box_bytes;
-#pragma unroll
-          for (int x = 0; x < C::kSub; ++x)
-            tma_load_2d(dst + x * kSubTile, host ? &maps.v_host : &maps.v_dev, 64 * x, y, vb);
+        if (++stage == stages) {
+          stage = 0;
+          parity ^= 1u;
         }
-        rv.next<C::kStagesV>();
       }
       // copies still in flight after a wait ran out get a bounded time to land
       // before the block's shared memory is released (a barrier's completed
       // phase is the parity before the next use's)
       if (*reinterpret_cast<volatile int32_t*>(&t.broken)) {
-        Ring ek = rk, ev = rv;
-        for (int i = 0; i < C::kStagesK; ++i, ek.next<C::kStagesK>())
-          mbar_wait_bounded(smem_u32(&t.k_full[ek.stage]), ek.parity ^ 1u);
-        for (int i = 0; i < C::kStagesV; ++i, ev.next<C::kStagesV>())
-          mbar_wait_bounded(smem_u32(&t.v_full[ev.stage]), ev.parity ^ 1u);
+        for (int i = 0; i < stages; ++i) {
+          mbar_wait_bounded(smem_u32(&full[stage]), parity ^ 1u);
+          if (++stage == stages) {
+            stage = 0;
+            parity ^= 1u;
+          }
+        }
       }
     } else if (warp == 1) {
       // ------------------------------------------------------------ matrix products
@@ -610,7 +619,6 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
     // -------------------------------------------------------------- softmax, a thread per row
-    const int r = tid & 127;
     if (m < num_m) {
       // The warp's 32 queries: rotated, to their place in the swizzled tile; rows
       // past the end are zero.  A lane takes 8 pairs of every kPer-th row (one
@@ -626,11 +634,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
 #pragma unroll
         for (int i = 0; i < kC; ++i) {
           const int id = first_row + kPer * i, tk = id >> p.group_shift;
-          const long long rw = static_cast<long long>(q0) + tk;
           ux[i] = uy[i] = make_uint4(0u, 0u, 0u, 0u);
-          if (tk < n && rw >= 0 && rw < p.total_rows) {
-            const uint16_t* const src = p.q + rw * p.q_stride +
-                                        static_cast<size_t>((h << p.group_shift) + (id & ((1 << p.group_shift) - 1))) * D + 8 * c;
+          if (tk < n_rows) {
+            const uint16_t* const src = p.q + (q0 + tk) * p.q_stride +
+                                        ((h << p.group_shift) + (id & ((1 << p.group_shift) - 1))) * D + 8 * c;
             ux[i] = *reinterpret_cast<const uint4*>(src);
             uy[i] = *reinterpret_cast<const uint4*>(src + D / 2);
           }
@@ -778,16 +785,14 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       auto flush = [&](auto bytes, auto&& place) {   // the warp's 32 rows of `bytes` bytes to place(row of the warp)
         constexpr int kRow = decltype(bytes)::value, kC = kRow / 16, kPer = 32 / kC;
         __syncwarp();
-#pragma unroll
+#pragma unroll 4
         for (int i = 0; i < kC; ++i) {
           const int r = kPer * i + lane / kC, c = lane % kC;
           const int id = row0 + 128 * m + 32 * (warp & 3) + r, tk = id >> p.group_shift;
-          const long long rw = static_cast<long long>(q0) + tk;
-          if (tk < n && rw >= 0 && rw < p.total_rows) {
-            const size_t at = static_cast<size_t>(rw) * p.hq + (h << p.group_shift) + (id & ((1 << p.group_shift) - 1));
-            reinterpret_cast<uint4*>(place(at))[c] =
+          if (tk < n_rows)
+            reinterpret_cast<uint4*>(
+                place(static_cast<size_t>(q0 + tk) * p.hq + ((h << p.group_shift) + (id & ((1 << p.group_shift) - 1)))))[c] =
                 *reinterpret_cast<const uint4*>(buf + r * kRow + ((c ^ (r & 7)) << 4));
-          }
         }
       };
       if (ok) {
@@ -820,9 +825,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       if (ok && p.nsplit == 1) flush(std::integral_constant<int, D * 2>{}, [&](size_t at) { return p.out + at * D; });
       if (ok && p.nsplit > 1)
         flush(std::integral_constant<int, D * 4>{}, [&](size_t at) { return p.part_o + (at * p.nsplit + split) * D; });
-      const size_t at = static_cast<size_t>(live ? row : 0) * p.hq + head;
       if (ok && live && p.nsplit > 1)
-        p.part_lse[at * p.nsplit + split] = nan ? __int_as_float(0x7fc00000) : (sum == 0.f ? -INFINITY : ref + __log2f(sum));
+        p.part_lse[place_of_row() * p.nsplit + split] = nan ? __int_as_float(0x7fc00000) : (sum == 0.f ? -INFINITY : ref + __log2f(sum));
     }
   }
   tmem_fence_before();

@@ -110,14 +110,16 @@ struct PrepareChunk {
 // Splits of every row tile's walk over the cache.  A CTA takes one (row tile,
 // kv head, split) and holds its SM; the time is the number of waves times a
 // CTA's share of the walk, plus about 3 tiles' time for its start and end and,
-// with splits, as much again for joining them.  `tiles` goes by the table's
-// capacity, as the lengths are on the device.
+// with splits, 2 for joining them (a tile takes 1.6 to 2.3 us).  `tiles` goes
+// by the table's capacity, as the lengths are on the device.  One sequence of
+// 64 rows on 4096 tokens: 70 us whole, 19 us in 16 to 32 splits; 8 rows on four
+// 64k contexts: 991 us whole, 263 us in 4, 251 us in 9, 298 us in 32.
 int chunk_splits(long long units, int sms, long long tiles, long long max_splits) {
   int best = 1;
   double best_cost = 0.0;
-  for (int n = 1; n <= 64 && n <= max_splits && (n == 1 || 2 * n <= tiles); ++n) {
+  for (int n = 1; n <= 64 && n <= max_splits && (n == 1 || n <= tiles); ++n) {
     const double waves = static_cast<double>((units * n + sms - 1) / sms);
-    const double cost = waves * (static_cast<double>((tiles + n - 1) / n) + 3.0) + (n > 1 ? 3.0 : 0.0);
+    const double cost = waves * (static_cast<double>((tiles + n - 1) / n) + 3.0) + (n > 1 ? 2.0 : 0.0);
     if (n == 1 || cost < 0.97 * best_cost) {
       best = n;
       best_cost = cost;
