@@ -92,6 +92,7 @@ struct dkv_handle {
   cudaEvent_t ev_join = nullptr;
   dkv::SplitEntry host_kernel{}, dev_kernel{}, dev_tma_kernel{}, multi_kernel{};  // dev: cp.async; dev_tma: tensor copies
   dkv::SplitEntry window_kernel{};
+  int window_ctas = 0;         // CTAs of the windowed kernel that one wave holds
   // tensor maps of the last device pool and staging pool the HBM kernel read
   struct PoolMaps {
     const void* k = nullptr;
