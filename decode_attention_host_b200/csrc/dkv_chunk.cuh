@@ -53,6 +53,7 @@ constexpr int kRegsIssue = 64;
 constexpr int kRegsRotate = 96;
 constexpr int kRegsSoftmax = 176;
 static_assert(kRegsIssue + kRegsRotate + 2 * kRegsSoftmax <= 4 * kRegsLaunch, "setmaxnreg.inc would wait for ever");
+constexpr float kMostOperand = 65504.f;            // fp16's largest value
 constexpr int kStatusRange = 64;                   // DKV_STATUS_RANGE
 
 struct ChunkParams {
@@ -282,9 +283,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     return;
   }
 
-  // ---- which rows: CTA = (row tile, kv head, split), the row tiles counted
-  // from the last one of the last sequence, as the last rows of a chunk see
-  // the most tokens
+  // ---- which rows: CTA = (row tile, kv head, split).  CTAs start in order, so
+  // the long ones come first: of up to 32 sequences the one that ends last (in
+  // tokens) first, and of a sequence its last row tile first, as that sees the
+  // most tokens.  More sequences are taken from the last one on.
   const int unit = p.div_split.div(static_cast<int>(blockIdx.x));
   const int split = static_cast<int>(blockIdx.x) - unit * p.nsplit;
   const int slot = p.div_hkv.div(unit);
@@ -297,13 +299,23 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       const int q = b >= 0 ? p.q_start[b] : 0;
       const int n = b >= 0 ? p.q_start[b + 1] - q : 0;
       const int len = b >= 0 ? p.seq_lens[b] : 0;
+      const bool rank = p.batch <= 32;
       const int tiles =
           n > 0 ? static_cast<int>(((static_cast<long long>(n) << p.group_shift) + kChunkRows - 1) / kChunkRows) : 0;
       int inc = tiles;
+      if (rank) {   // row tiles of this sequence and of those before it in the order
+        const unsigned key = static_cast<unsigned>(max(len, 0)) + static_cast<unsigned>(max(n, 0));
+        for (int o = 0; o < p.batch; ++o) {
+          const unsigned other = __shfl_sync(kFull, key, o);
+          const int more = __shfl_sync(kFull, tiles, o);
+          if (other > key || (other == key && o < lane)) inc += more;
+        }
+      } else {
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int u = __shfl_up_sync(kFull, inc, o);
-        if (lane >= o) inc += u;
+        for (int o = 1; o < 32; o <<= 1) {
+          const int u = __shfl_up_sync(kFull, inc, o);
+          if (lane >= o) inc += u;
+        }
       }
       const unsigned hit = __ballot_sync(kFull, slot < before + inc && slot >= before + inc - tiles);
       if (hit) {
@@ -568,7 +580,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       if (!__all_sync(kFull, chunk_wait(&t.k_full[rk.stage], rk.parity, t, p.status))) break;
       if constexpr (ROPE) {
         char* const k = sk + rk.stage * C::kTile;
-        uint32_t mx = 0;
+        float mx = 0.f;
 #pragma unroll
         for (int i = 0; i < 128 / kStep; ++i) {
           const int rw = rr + kStep * i;
@@ -589,12 +601,15 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
           const int tt = p0 + rw;
           if (!edge || (tt < hi_max && (tt >= lo_min || tt < sk_end))) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) mx = hmax_abs2(mx, o[e]);
+            for (int e = 0; e < 4; ++e) {
+              mx = fmaxf(mx, fmaxf(fabsf(X[e].x), fabsf(X[e].y)));
+              mx = fmaxf(mx, fmaxf(fabsf(Y[e].x), fabsf(Y[e].y)));
+            }
           }
           *px = make_uint4(o[0], o[1], o[2], o[3]);
           *py = make_uint4(o[4], o[5], o[6], o[7]);
         }
-        if (has_inf2(mx)) {
+        if (mx > kMostOperand) {
           *reinterpret_cast<volatile int32_t*>(&t.poison) = 1;
           atomicOr(p.status, kStatusRange);
         }
