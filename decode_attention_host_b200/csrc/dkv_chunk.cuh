@@ -42,7 +42,6 @@
 namespace dkv {
 
 constexpr int kChunkTokens = 128;                  // tokens of a K/V tile, the N of S = Q K^T
-constexpr int kChunkRows = 256;                    // rows of a CTA: two tiles of 128
 constexpr int kChunkThreads = 512;
 constexpr int kSubTile = kChunkTokens * 128;       // bytes of 128 rows x 64 elements, 128-byte swizzle
 constexpr int kRopeChain = 8;                      // K tiles that may follow one seed of the rotation
@@ -89,6 +88,7 @@ struct ChunkShape {
   static constexpr int kTile = kSub * kSubTile;             // bytes of a Q, K or V tile
   static constexpr int kStagesK = D == 128 ? 3 : 4;
   static constexpr int kStagesV = D == 128 ? 2 : 4;
+  static constexpr int kMoreV = D == 128 ? 1 : 0;            // in the place of an unused second Q tile
 };
 
 struct ChunkTail {
@@ -265,16 +265,25 @@ struct Ring {
 
 // ----------------------------------------------------------------------------- the kernel
 
-template <int D, bool BF16, bool ROPE>
+// DUAL: a CTA takes 128 rows instead of 256.  Both softmax groups and both halves
+// of TMEM then serve the same rows: the first has the even K/V tiles, the second
+// the odd ones, and their results are joined at the end.  A group's tile goes
+// through product, softmax and product in turn, so with one group alone the
+// tensor core and the copies idle most of the time (8 rows on four 64k contexts:
+// 243 us, 201 with two).
+template <int D, bool BF16, bool ROPE, bool DUAL>
 __global__ void __launch_bounds__(kChunkThreads, 1)
     chunk_kernel(const ChunkParams p, const __grid_constant__ ChunkMaps maps) {
   using C = ChunkShape<D>;
+  constexpr int kRows = DUAL ? 128 : 256;    // rows of a CTA
+  constexpr int kStagesV = C::kStagesV + (DUAL ? C::kMoreV : 0);
   constexpr bool kOpBf16 = BF16 && !ROPE;    // type of the Q K^T operands
   extern __shared__ __align__(1024) char chunk_smem[];
   char* const sq = chunk_smem;
-  char* const sk = sq + 2 * C::kTile;
-  char* const sv = sk + C::kStagesK * C::kTile;
-  ChunkTail& t = *reinterpret_cast<ChunkTail*>(sv + C::kStagesV * C::kTile);
+  // V's stages follow the two Q tiles, the second of which is one more of them under DUAL
+  char* const sv = sq + (DUAL && C::kMoreV ? 1 : 2) * C::kTile;
+  char* const sk = sv + kStagesV * C::kTile;
+  ChunkTail& t = *reinterpret_cast<ChunkTail*>(sk + C::kStagesK * C::kTile);
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(kFull, tid >> 5, 0);   // warp-uniform, and known to be
 
@@ -301,7 +310,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       const int len = b >= 0 ? p.seq_lens[b] : 0;
       const bool rank = p.batch <= 32;
       const int tiles =
-          n > 0 ? static_cast<int>(((static_cast<long long>(n) << p.group_shift) + kChunkRows - 1) / kChunkRows) : 0;
+          n > 0 ? static_cast<int>(((static_cast<long long>(n) << p.group_shift) + kRows - 1) / kRows) : 0;
       int inc = tiles;
       if (rank) {   // row tiles of this sequence and of those before it in the order
         const unsigned key = static_cast<unsigned>(max(len, 0)) + static_cast<unsigned>(max(n, 0));
@@ -358,9 +367,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   const int b = t.b;
   if (b < 0) return;
   const int q0 = t.q0, n = t.n, L = t.len;
-  const int row0 = t.tile * kChunkRows;
-  const int rows = min((n << p.group_shift) - row0, kChunkRows);
-  const int num_m = rows > 128 ? 2 : 1;
+  const int row0 = t.tile * kRows;
+  const int rows = min((n << p.group_shift) - row0, kRows);
   const bool bad_len = L < 0 || L > p.max_len - n;
 
   // ---- which tokens: [0, sk_end) and [lo_min, hi_max), in tiles of 128
@@ -376,9 +384,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   const int nt = min(j0 + per, total) - j0;
   auto tile_pos = [&](int j) { return (j0 + j < na ? j0 + j : tb + j0 + j - na) * kChunkTokens; };
 
-  // output of this thread's row (softmax warps: row tile `m`)
-  const int m = (warp >> 2) - 2;                 // softmax: row tile 0 or 1
-  const int idx = row0 + (tid & 255);            // threads 256..511 own rows 0..255
+  // this thread's row (softmax warps)
+  const int m = (warp >> 2) - 2;                 // softmax: group 0 or 1
+  const int row_m = row0 + (DUAL ? 0 : 128 * m); // first row of the group's row tile
+  const int idx = row_m + (tid & 127);
   const int tok = idx >> p.group_shift;
   const int head = (h << p.group_shift) + (idx & ((1 << p.group_shift) - 1));
   // tokens whose rows exist: all n, unless q_start names rows outside the buffers
@@ -420,10 +429,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       // the rotated key tile came last and set the pace, 4280 cycles a tile).
       // The block ids of the next tile are read while this one's stage is waited for.
       const bool is_v = warp == 2;
-      const int stages = is_v ? C::kStagesV : C::kStagesK;
+      const int stages = is_v ? kStagesV : C::kStagesK;
       uint64_t* const full = is_v ? t.v_full : t.k_full;
       uint64_t* const free_ = is_v ? t.v_free : t.k_free;
-      char* const tiles = is_v ? sv : sk;
       const CUtensorMap* const dev_map = is_v ? &maps.v_dev : &maps.k_dev;
       const CUtensorMap* const host_map = is_v ? &maps.v_host : &maps.k_host;
       const int nbox = kChunkTokens / p.box;
@@ -457,7 +465,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         if (lane == 0) mbar_arrive_expect_tx(bar, C::kTile);
         __syncwarp();
         if (lane < nbox) {
-          const uint32_t dst = smem_u32(tiles + stage * C::kTile) + lane * box_bytes;
+          const uint32_t dst = smem_u32((is_v ? sv : sk) + stage * C::kTile) + lane * box_bytes;
 #pragma unroll
           for (int x = 0; x < C::kSub; ++x) tma_load_2d(dst + x * kSubTile, host ? host_map : dev_map, 64 * x, y, bar);
         }
@@ -487,53 +495,84 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       constexpr uint32_t kIdQK = umma_idesc(128, kChunkTokens, kOpBf16, false);
       constexpr uint32_t kIdPV = umma_idesc(128, D, BF16, true);
       const uint32_t on = lane == 0;
-      const int tiles = __shfl_sync(kFull, nt, 0), row_tiles = __shfl_sync(kFull, num_m, 0);
+      const int tiles = __shfl_sync(kFull, nt, 0);
       const uint32_t tm = __shfl_sync(kFull, *reinterpret_cast<volatile uint32_t*>(&t.tmem), 0);
       const uint32_t q_low = desc_low(smem_u32(sq), 16), k_low = desc_low(smem_u32(sk), 16);
       const uint32_t v_low = desc_low(smem_u32(sv), kSubTile);
-      auto qk = [&](int mt, int stage) {   // S = Q K^T, both K-major
-        const uint32_t a = q_low + mt * (C::kTile >> 4), k = k_low + stage * (C::kTile >> 4);
+      // S of group g = Q K^T, both K-major
+      auto qk = [&](int g, uint32_t a, int stage) {
+        const uint32_t k = k_low + stage * (C::kTile >> 4);
 #pragma unroll
         for (int i = 0; i < D / 16; ++i) {
           const uint32_t o = ((i >> 2) * kSubTile + (i & 3) * 32) >> 4;
-          umma_ss(tm + 128 * mt, a + o, k + o, kIdQK, i > 0, on);
+          umma_ss(tm + 128 * g, a + o, k + o, kIdQK, i > 0, on);
         }
-        umma_commit(smem_u32(&t.s_full[mt]), on);
+        umma_commit(smem_u32(&t.s_full[g]), on);
       };
-      auto pv = [&](int mt, int stage, bool acc) {   // O += P V: V is N-major, 64-column blocks kSubTile apart
-        const uint32_t v = v_low + stage * (C::kTile >> 4), pw = tm + 128 * mt;
+      // O of group g += P V: V is N-major, 64-column blocks kSubTile apart
+      auto pv = [&](int g, uint32_t v, bool acc) {
 #pragma unroll
         for (int i = 0; i < kChunkTokens / 16; ++i)
-          umma_ts(tm + 256 + D * mt, pw + 8 * i, v + i * (2048 >> 4), kIdPV, acc || i > 0, on);
+          umma_ts(tm + 256 + D * g, tm + 128 * g + 8 * i, v + i * (2048 >> 4), kIdPV, acc || i > 0, on);
       };
       Ring rk, rv;
-      bool ok = true;
-      for (int i = 0; i < row_tiles; ++i) ok = ok && chunk_wait(&t.q_ready[i], 0, t, p.status);
+      bool ok = chunk_wait(&t.q_ready[0], 0, t, p.status);
+      const int row_tiles = __shfl_sync(kFull, rows > 128 ? 2 : 1, 0);
+      if (!DUAL && row_tiles == 2) ok = ok && chunk_wait(&t.q_ready[1], 0, t, p.status);
       ok = ok && chunk_wait(&t.k_ready[0], 0, t, p.status);
-      if (__all_sync(kFull, ok)) {
+      ok = __all_sync(kFull, ok);
+      if (!DUAL && ok) {
+        // two row tiles (or one, if no rows are left for the second): each K/V tile
+        // is group 0's turn, then group 1's; a group's next S is issued right
+        // behind its O
         tmem_fence_after();
-        for (int i = 0; i < row_tiles; ++i) qk(i, 0);
+        qk(0, q_low, 0);
+        if (row_tiles == 2) qk(1, q_low + (C::kTile >> 4), 0);
         umma_commit(smem_u32(&t.k_free[0]), on);
         rk.next<C::kStagesK>();
         for (int j = 0; j < tiles; ++j) {
           const bool more = j + 1 < tiles;
           ok = __all_sync(kFull, chunk_wait(&t.v_full[rv.stage], rv.parity, t, p.status));
-          for (int i = 0; i < row_tiles && ok; ++i) {
-            ok = chunk_wait(&t.p_ready[i], j & 1, t, p.status);
-            if (i == 0 && more) ok = ok && chunk_wait(&t.k_ready[rk.stage], rk.parity, t, p.status);
+#pragma unroll 1   // unrolled, its operands no longer fit in uniform registers: 4% slower
+          for (int g = 0; g < row_tiles && ok; ++g) {
+            ok = chunk_wait(&t.p_ready[g], j & 1, t, p.status);
+            if (g == 0 && more) ok = ok && chunk_wait(&t.k_ready[rk.stage], rk.parity, t, p.status);
             if (!(ok = __all_sync(kFull, ok))) break;
             tmem_fence_after();
-            pv(i, rv.stage, j > 0);
-            if (i == row_tiles - 1) umma_commit(smem_u32(&t.v_free[rv.stage]), on);
+            pv(g, v_low + rv.stage * (C::kTile >> 4), j > 0);
+            if (g == row_tiles - 1) umma_commit(smem_u32(&t.v_free[rv.stage]), on);
             if (more) {
-              qk(i, rk.stage);
-              if (i == row_tiles - 1) umma_commit(smem_u32(&t.k_free[rk.stage]), on);
+              qk(g, q_low + g * (C::kTile >> 4), rk.stage);
+              if (g == row_tiles - 1) umma_commit(smem_u32(&t.k_free[rk.stage]), on);
             }
             __syncwarp();
           }
           if (!ok) break;
-          rv.next<C::kStagesV>();
+          rv.next<kStagesV>();
           rk.next<C::kStagesK>();
+        }
+      } else if (DUAL && ok) {
+        // one row tile: K/V tile j is group (j mod 2)'s turn, tile j + 2 its next
+        auto next_s = [&](int j) {
+          if (!__all_sync(kFull, chunk_wait(&t.k_ready[rk.stage], rk.parity, t, p.status))) return false;
+          tmem_fence_after();
+          qk(j & 1, q_low, rk.stage);
+          umma_commit(smem_u32(&t.k_free[rk.stage]), on);
+          rk.next<C::kStagesK>();
+          return true;
+        };
+        ok = next_s(0) && (tiles == 1 || next_s(1));
+#pragma unroll 1
+        for (int j = 0; j < tiles && ok; ++j) {
+          ok = chunk_wait(&t.v_full[rv.stage], rv.parity, t, p.status);
+          ok = ok && chunk_wait(&t.p_ready[j & 1], (j >> 1) & 1, t, p.status);
+          if (!(ok = __all_sync(kFull, ok))) break;
+          tmem_fence_after();
+          pv(j & 1, v_low + rv.stage * (C::kTile >> 4), j > 1);
+          umma_commit(smem_u32(&t.v_free[rv.stage]), on);
+          rv.next<kStagesV>();
+          if (j + 2 < tiles) ok = next_s(j + 2);
+          __syncwarp();
         }
       }
       // also after a wait ran out: what was issued completes before TMEM is given back
@@ -629,21 +668,21 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&t.k_ready[rk.stage]));
       rk.next<C::kStagesK>();
-      rv.next<C::kStagesV>();
+      rv.next<kStagesV>();
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
     // -------------------------------------------------------------- softmax, a thread per row
-    if (m < num_m) {
+    if (DUAL || m == 0 || rows > 128) {
       // The warp's 32 queries: rotated, to their place in the swizzled tile; rows
       // past the end are zero.  A lane takes 8 pairs of every kPer-th row (one
       // 16-byte chunk of each half), so that a load covers whole lines, and its
       // cos / sin advance from row to row as those of the keys do.
       const int pos = L + tok;
-      {
+      if (!DUAL || m == 0) {
         constexpr int kC = D / 16, kPer = 32 / kC;
         const int c = lane % kC, r0 = 32 * (warp & 3) + lane / kC;
-        const int first_row = row0 + 128 * m + r0;
+        const int first_row = row_m + r0;
         const int step = kPer >> p.group_shift;
         uint4 ux[kC], uy[kC];   // every load in flight at once: the first product waits for the last
 #pragma unroll
@@ -702,15 +741,16 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       const int hi = live ? pos + p.self : 0;
       const int lo = p.window ? max(0, hi - p.window) : 0;
       // the row tile's tightest bounds: a K/V tile inside them needs no mask
-      const int first = L + ((row0 + 128 * m) >> p.group_shift) + p.self;
-      const int last = L + ((row0 + min(rows, 128 * m + 128) - 1) >> p.group_shift) + p.self;
+      const int first = L + (row_m >> p.group_shift) + p.self;
+      const int last = L + (min(row0 + rows, row_m + 128) - 1 >> p.group_shift) + p.self;
       const int lo_last = p.window ? max(0, last - p.window) : 0;
       const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
       uint32_t ts = 0, to = 0;
       float ref = -1e30f, sum = 0.f;
       bool ok = true;
-      for (int j = 0; j < nt; ++j) {
-        const int p0 = tile_pos(j);
+      const int turns = DUAL ? (nt + 1 - m) >> 1 : nt;
+      for (int j = 0; j < turns; ++j) {
+        const int p0 = tile_pos(DUAL ? 2 * j + m : j);
         ok = __all_sync(kFull, chunk_wait(&t.s_full[m], j & 1, t, p.status));
         if (!ok) break;
         tmem_fence_after();
@@ -791,31 +831,72 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       ok = ok && __all_sync(kFull, chunk_wait(&t.done, 0, t, p.status));
       tmem_fence_after();
       // ---- the row's result
-      const bool nan = !ok || *reinterpret_cast<volatile int32_t*>(&t.poison);
-      const float inv = nan ? __int_as_float(0x7fc00000) : (sum == 0.f ? 0.f : 1.f / sum);
       // A thread's row goes through the block's shared memory, which nothing reads
       // any more, so that the warp writes whole lines: row by row from the
       // threads themselves, a CTA's 256 rows of fp32 took 10,600 cycles.
       char* const buf = chunk_smem + (warp - 8) * (32 * D * 4);
+      float2* const other = reinterpret_cast<float2*>(chunk_smem + 8 * (32 * D * 4));   // the second group's (ref, sum)
+      float mine = 1.f, theirs = 0.f;   // factors of the two groups' O
+      if (DUAL) {
+        if (m == 1) {
+          if (ok && turns > 0) {
+#pragma unroll 1
+            for (int i = 0; i < D / 32; ++i) {
+              uint32_t o[32];
+              tmem_ld32(to + 32 * i, o);
+              tmem_ld_wait(o);
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                *reinterpret_cast<uint4*>(buf + lane * (D * 4) + (((8 * i + e) ^ (lane & 7)) << 4)) =
+                    make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+            }
+            other[tid & 127] = make_float2(ref, sum);
+          }
+        }
+        asm volatile("bar.sync 1, 256;" ::: "memory");   // both groups come here, after a wait that ran out too
+        if (m == 0 && nt > 1 && ok) {
+          const float2 o = other[tid & 127];
+          const float top = fmaxf(ref, o.x);
+          mine = ex2(ref - top);
+          theirs = ex2(o.x - top);
+          sum = sum * mine + o.y * theirs;
+          ref = top;
+        }
+      }
+      ok = ok && *reinterpret_cast<volatile int32_t*>(&t.broken) == 0;
+      const bool nan = !ok || *reinterpret_cast<volatile int32_t*>(&t.poison);
+      const float inv = nan ? __int_as_float(0x7fc00000) : (sum == 0.f ? 0.f : 1.f / sum);
       auto flush = [&](auto bytes, auto&& place) {   // the warp's 32 rows of `bytes` bytes to place(row of the warp)
         constexpr int kRow = decltype(bytes)::value, kC = kRow / 16, kPer = 32 / kC;
         __syncwarp();
 #pragma unroll 4
         for (int i = 0; i < kC; ++i) {
           const int r = kPer * i + lane / kC, c = lane % kC;
-          const int id = row0 + 128 * m + 32 * (warp & 3) + r, tk = id >> p.group_shift;
+          const int id = row_m + 32 * (warp & 3) + r, tk = id >> p.group_shift;
           if (tk < n_rows)
             reinterpret_cast<uint4*>(
                 place(static_cast<size_t>(q0 + tk) * p.hq + ((h << p.group_shift) + (id & ((1 << p.group_shift) - 1)))))[c] =
                 *reinterpret_cast<const uint4*>(buf + r * kRow + ((c ^ (r & 7)) << 4));
         }
       };
-      if (ok) {
+      const bool writes = !DUAL || m == 0;
+      if (ok && writes) {
 #pragma unroll 1
         for (int i = 0; i < D / 32; ++i) {
           uint32_t o[32];
           tmem_ld32(to + 32 * i, o);
           tmem_ld_wait(o);
+          if (DUAL && nt > 1) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const float4 x = *reinterpret_cast<const float4*>(buf + 4 * (32 * D * 4) + lane * (D * 4) +
+                                                                 (((8 * i + e) ^ (lane & 7)) << 4));
+              o[4 * e] = __float_as_uint(__uint_as_float(o[4 * e]) * mine + x.x * theirs);
+              o[4 * e + 1] = __float_as_uint(__uint_as_float(o[4 * e + 1]) * mine + x.y * theirs);
+              o[4 * e + 2] = __float_as_uint(__uint_as_float(o[4 * e + 2]) * mine + x.z * theirs);
+              o[4 * e + 3] = __float_as_uint(__uint_as_float(o[4 * e + 3]) * mine + x.w * theirs);
+            }
+          }
           if (p.nsplit == 1) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
@@ -834,13 +915,13 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                               __uint_as_float(o[4 * e + 2]) * inv, __uint_as_float(o[4 * e + 3]) * inv);
           }
         }
-      } else {   // a wait ran out: copies may still be landing in shared memory
+      } else if (!ok) {   // a wait ran out: copies may still be landing in shared memory
         one_value(true);
       }
-      if (ok && p.nsplit == 1) flush(std::integral_constant<int, D * 2>{}, [&](size_t at) { return p.out + at * D; });
-      if (ok && p.nsplit > 1)
+      if (ok && writes && p.nsplit == 1) flush(std::integral_constant<int, D * 2>{}, [&](size_t at) { return p.out + at * D; });
+      if (ok && writes && p.nsplit > 1)
         flush(std::integral_constant<int, D * 4>{}, [&](size_t at) { return p.part_o + (at * p.nsplit + split) * D; });
-      if (ok && live && p.nsplit > 1)
+      if (ok && writes && live && p.nsplit > 1)
         p.part_lse[place_of_row() * p.nsplit + split] = nan ? __int_as_float(0x7fc00000) : (sum == 0.f ? -INFINITY : ref + __log2f(sum));
     }
   }

@@ -41,8 +41,10 @@ dkv::SplitEntry window_entry() {
 }
 
 template <int D, bool BF16, bool ROPE>
-cudaError_t launch_chunk(cudaStream_t s, const dkv::ChunkParams& p, const dkv::ChunkMaps& m, int ctas) {
-  dkv::chunk_kernel<D, BF16, ROPE><<<ctas, dkv::kChunkThreads, dkv::chunk_smem_bytes<D>(), s>>>(p, m);
+cudaError_t launch_chunk(cudaStream_t s, const dkv::ChunkParams& p, const dkv::ChunkMaps& m, int ctas,
+                         int rows) {
+  if (rows == 128) dkv::chunk_kernel<D, BF16, ROPE, true><<<ctas, dkv::kChunkThreads, dkv::chunk_smem_bytes<D>(), s>>>(p, m);
+  else dkv::chunk_kernel<D, BF16, ROPE, false><<<ctas, dkv::kChunkThreads, dkv::chunk_smem_bytes<D>(), s>>>(p, m);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || p.nsplit == 1) return e;
   cudaLaunchConfig_t cfg{};
@@ -57,9 +59,9 @@ cudaError_t launch_chunk(cudaStream_t s, const dkv::ChunkParams& p, const dkv::C
   return cudaLaunchKernelEx(&cfg, dkv::chunk_merge_kernel<D, BF16>, p);
 }
 
-template <int D, bool BF16, bool ROPE>
+template <int D, bool BF16, bool ROPE, bool DUAL>
 cudaError_t prepare_chunk() {
-  auto* const k = dkv::chunk_kernel<D, BF16, ROPE>;
+  auto* const k = dkv::chunk_kernel<D, BF16, ROPE, DUAL>;
   cudaFuncAttributes a{};
   cudaError_t e = cudaFuncGetAttributes(&a, k);
   if (e != cudaSuccess) return e;
@@ -99,32 +101,36 @@ struct LaunchChunk {
   cudaStream_t s;
   const dkv::ChunkParams& p;
   const dkv::ChunkMaps& m;
-  int ctas;
+  int ctas, rows;
   template <int D, int G, bool BF16, bool ROPE>
   cudaError_t operator()() const {
-    return launch_chunk<D, BF16, ROPE>(s, p, m, ctas);
+    return launch_chunk<D, BF16, ROPE>(s, p, m, ctas, rows);
   }
 };
 struct PrepareChunk {
   template <int D, int G, bool BF16, bool ROPE>
   cudaError_t operator()() const {
-    return prepare_chunk<D, BF16, ROPE>();
+    const cudaError_t e = prepare_chunk<D, BF16, ROPE, false>();
+    return e != cudaSuccess ? e : prepare_chunk<D, BF16, ROPE, true>();
   }
 };
 
 // Splits of every row tile's walk over the cache.  A CTA takes one (row tile,
 // kv head, split) and holds its SM; the time is the number of waves times a
-// CTA's share of the walk, plus about 3 tiles' time for its start and end and,
-// with splits, 2 for joining them (a tile takes 1.6 to 2.3 us).  `tiles` goes
-// by the table's capacity, as the lengths are on the device.  One sequence of
-// 64 rows on 4096 tokens: 70 us whole, 19 us in 16 to 32 splits; 8 rows on four
-// 64k contexts: 991 us whole, 263 us in 4, 251 us in 9, 298 us in 32.
-int chunk_splits(long long units, int sms, long long tiles, long long max_splits) {
+// CTA's share of the walk and its start and end, about 10 us, which is 12
+// tiles' time with 128 rows to a CTA (0.8 us a tile) and 5 with 256 (2 us),
+// and about one tile's for joining.  `tiles` goes by the table's capacity, as
+// the lengths are on the device.  16 rows of 4 heads on 4096 tokens: 40 us
+// whole, 17 in 5 splits, 14.5 in 9 to 32; 8 sequences of 16 rows of 32 heads:
+// 62 us whole, 43 in 2 (one wave), 55 in 4; 8 rows of 32 heads on four 64k
+// contexts: 201 in 4 or 9, 338 in 2, 264 in 32.
+int chunk_splits(long long units, int sms, long long tiles, int rows, long long max_splits) {
+  const double ends = rows == 128 ? 12.0 : 5.0;
   int best = 1;
   double best_cost = 0.0;
   for (int n = 1; n <= 64 && n <= max_splits && (n == 1 || n <= tiles); ++n) {
     const double waves = static_cast<double>((units * n + sms - 1) / sms);
-    const double cost = waves * (static_cast<double>((tiles + n - 1) / n) + 3.0) + (n > 1 ? 2.0 : 0.0);
+    const double cost = waves * (static_cast<double>((tiles + n - 1) / n) + ends) + (n > 1 ? 1.0 : 0.0);
     if (n == 1 || cost < 0.97 * best_cost) {
       best = n;
       best_cost = cost;
@@ -345,15 +351,20 @@ int dkv_attn_chunk(dkv_handle* h, const void* q, int64_t q_stride, const int32_t
   p.sinks = window ? sinks : 0;
   p.self = include_self;
   p.qscale = h->qscale;
-  // sum over b of ceil(rows_b G / 256), rows_b unknown here, is at most this
+  // 128 rows to a CTA while a sequence has no more of them on average (a kv head's rows: its tokens times G)
+  const int rows = static_cast<long long>(total_rows) * h->G <= 128LL * batch ? 128 : 256;
+  // sum over b of ceil(rows_b G / rows), rows_b unknown here, is at most this
   const long long row_tiles =
-      (static_cast<long long>(total_rows) * h->G + static_cast<long long>(batch) * (dkv::kChunkRows - h->G)) /
-      dkv::kChunkRows;
+      (static_cast<long long>(total_rows) * h->G + static_cast<long long>(batch) * (rows - h->G)) / rows;
   const long long units = row_tiles * c.num_kv_heads;
   long long see = p.max_len;   // tokens that a row tile may walk over
-  if (window && static_cast<long long>(window) + sinks + 2 * dkv::kChunkRows < see)
-    see = static_cast<long long>(window) + sinks + 2 * dkv::kChunkRows;
-  p.nsplit = chunk_splits(units, h->sm_count, (see + dkv::kChunkTokens - 1) / dkv::kChunkTokens,
+  if (window && static_cast<long long>(window) + sinks + 512 < see)
+    see = static_cast<long long>(window) + sinks + 512;
+  // the plan counts the row tiles to expect: one for each sequence, or as many
+  // as the rows fill and half a tile more for each sequence's last one
+  const long long fill = static_cast<long long>(total_rows) * h->G / rows + batch / 2;
+  const long long expect = fill < batch ? batch : fill > row_tiles ? row_tiles : fill;
+  p.nsplit = chunk_splits((expect < row_tiles ? expect : row_tiles) * c.num_kv_heads, h->sm_count, (see + dkv::kChunkTokens - 1) / dkv::kChunkTokens, rows,
                           static_cast<long long>(h->part_rows) / (static_cast<long long>(total_rows) * c.num_q_heads));
   if (units * p.nsplit > INT_MAX) return set_error(DKV_ERR_INVALID_ARG, "dkv_attn_chunk: too many rows");
   p.div_bs = dkv::make_invdiv(c.block_size);
@@ -378,7 +389,7 @@ int dkv_attn_chunk(dkv_handle* h, const void* q, int64_t q_stride, const int32_t
   }
   if (code != 0)
     return set_error(DKV_ERR_CUDA, "cuTensorMapEncodeTiled rejected the pool's tensor map (" + std::to_string(code) + ")");
-  DKV_CUDA(by_shape(c, LaunchChunk{s, p, maps, static_cast<int>(units * p.nsplit)}));
+  DKV_CUDA(by_shape(c, LaunchChunk{s, p, maps, static_cast<int>(units * p.nsplit), rows}));
   h->last_launches = p.nsplit > 1 ? 2 : 1;
   return DKV_OK;
 }
