@@ -444,6 +444,11 @@ class DecodeAttention:
         (q_start, slot_map); kv's table grows and free_count goes down in place, kv.seq_lens_dev stays."""
         import torch
         dev = new_lens.device
+        for x in (new_lens, free_ids, free_count):
+            if x.dtype != torch.int32 or not x.is_contiguous():
+                raise ValueError("new_lens, free_ids and free_count are contiguous int32 tensors")
+        if new_lens.numel() != kv.batch or free_count.numel() != 1:
+            raise ValueError("new_lens holds one length for each sequence, free_count one number")
         if stream is None:
             stream = torch.cuda.current_stream(dev)
         q_start = torch.empty(kv.batch + 1, dtype=torch.int32, device=dev)
@@ -456,17 +461,19 @@ class DecodeAttention:
         """Store k_new, v_new [rows, Hkv, D] (16-bit; rows may be strided, elements of a row are not) at slot_map."""
         import torch
         rows = k_new.shape[0]
+        width = kv.num_kv_heads * kv.head_dim
         for x in (k_new, v_new):
-            if x.shape != (rows, kv.num_kv_heads, kv.head_dim) or x.stride()[1:] != (kv.head_dim, 1):
-                raise ValueError("k_new and v_new are [rows, Hkv, D] with contiguous rows")
-        if k_new.stride(0) != v_new.stride(0):
+            if x.shape != (rows, kv.num_kv_heads, kv.head_dim) or x.element_size() != 2 or \
+                    (rows and x.stride()[1:] != (kv.head_dim, 1)):
+                raise ValueError("k_new and v_new are 16-bit [rows, Hkv, D] with contiguous rows")
+        if rows > 1 and k_new.stride(0) != v_new.stride(0):
             raise ValueError("k_new and v_new have one row stride")
-        if slot_map.numel() < rows:
-            raise ValueError("slot_map holds fewer slots than there are rows")
+        if slot_map.dtype != torch.int64 or not slot_map.is_contiguous() or slot_map.numel() < rows:
+            raise ValueError("slot_map is contiguous int64 with a slot for every row")
         if stream is None:
             stream = torch.cuda.current_stream(k_new.device)
-        dkv_store_kv(self.handle, k_new, v_new, k_new.stride(0), slot_map, rows, kv.host_split, kv.k_host.ptr or None,
-                     kv.v_host.ptr or None, kv.k_dev if kv.num_dev_blocks else None,
+        dkv_store_kv(self.handle, k_new, v_new, k_new.stride(0) if rows > 1 else width, slot_map, rows, kv.host_split,
+                     kv.k_host.ptr or None, kv.v_host.ptr or None, kv.k_dev if kv.num_dev_blocks else None,
                      kv.v_dev if kv.num_dev_blocks else None, stream.cuda_stream, kv.num_dev_blocks)
 
     def chunk(self, q, q_start, kv: PagedKV, out, window: int = 0, sinks: int = 0, include_self: bool = True,
@@ -475,11 +482,15 @@ class DecodeAttention:
         positions seq_lens[b] ..; causal over the cache, under a window of tokens and sinks if window > 0."""
         import torch
         hq, d = self.cfg.num_q_heads, self.cfg.head_dim
-        if q.shape[1:] != (hq, d) or q.stride()[1:] != (d, 1) or out.shape != q.shape or not out.is_contiguous():
-            raise ValueError("q is [rows, Hq, D] with contiguous rows, out the same and contiguous")
+        rows = q.shape[0]
+        if q.shape[1:] != (hq, d) or q.element_size() != 2 or (rows and q.stride()[1:] != (d, 1)) or \
+                out.shape != q.shape or out.dtype != q.dtype or not out.is_contiguous():
+            raise ValueError("q is 16-bit [rows, Hq, D] with contiguous rows, out the same and contiguous")
+        if q_start.dtype != torch.int32 or not q_start.is_contiguous() or q_start.numel() != kv.batch + 1:
+            raise ValueError("q_start is contiguous int32 [batch + 1]")
         if stream is None:
             stream = torch.cuda.current_stream(q.device)
-        dkv_attn_chunk(self.handle, q, max(q.stride(0), hq * d), q_start, q.shape[0], kv.k_host.ptr or None,
+        dkv_attn_chunk(self.handle, q, q.stride(0) if rows > 1 else hq * d, q_start, rows, kv.k_host.ptr or None,
                        kv.v_host.ptr or None, kv.k_dev if kv.num_dev_blocks else None,
                        kv.v_dev if kv.num_dev_blocks else None, kv.table_dev, kv.seq_lens_dev, kv.host_split, out,
                        window, sinks, include_self, stream.cuda_stream, kv.batch, kv.stride, kv.num_dev_blocks,

@@ -364,8 +364,9 @@ int dkv_attn_chunk(dkv_handle* h, const void* q, int64_t q_stride, const int32_t
   // as the rows fill and half a tile more for each sequence's last one
   const long long fill = static_cast<long long>(total_rows) * h->G / rows + batch / 2;
   const long long expect = fill < batch ? batch : fill > row_tiles ? row_tiles : fill;
-  p.nsplit = chunk_splits((expect < row_tiles ? expect : row_tiles) * c.num_kv_heads, h->sm_count, (see + dkv::kChunkTokens - 1) / dkv::kChunkTokens, rows,
-                          static_cast<long long>(h->part_rows) / (static_cast<long long>(total_rows) * c.num_q_heads));
+  const long long walk = (see + dkv::kChunkTokens - 1) / dkv::kChunkTokens;
+  const long long room = static_cast<long long>(h->part_rows) / (static_cast<long long>(total_rows) * c.num_q_heads);
+  p.nsplit = chunk_splits((expect < row_tiles ? expect : row_tiles) * c.num_kv_heads, h->sm_count, walk, rows, room);
   if (units * p.nsplit > INT_MAX) return set_error(DKV_ERR_INVALID_ARG, "dkv_attn_chunk: too many rows");
   p.div_bs = dkv::make_invdiv(c.block_size);
   p.div_hkv = dkv::make_invdiv(c.num_kv_heads);

@@ -285,8 +285,9 @@ DKV_API int dkv_store_kv(dkv_handle* h, const void* k_new, const void* v_new, in
  *   k_stage, v_stage  NULL, or device memory (HBM) of >= host_split blocks
  *                 each, pool layout, 16-byte aligned.  Without them
  *                 host-resident blocks are read in place over PCIe, once for
- *                 every 256 / (Hq/Hkv) rows of a chunk; with them the first
- *                 host_split blocks of the host pools are copied there first.
+ *                 each row tile (at most 256 / (Hq/Hkv) rows of a chunk); with
+ *                 them the first host_split blocks of the host pools are
+ *                 copied there first.
  * Scores, softmax statistics and outputs are accumulated in fp32; rotated
  * queries and keys are held in fp16 (|x| <= 65504 after rotation, else
  * DKV_STATUS_RANGE and NaN for the 256 / (Hq/Hkv) rows of the chunk that are
@@ -326,9 +327,11 @@ DKV_API int dkv_get_status(dkv_handle* h, int32_t* status);
 DKV_API const char* dkv_last_error_string(void);
 
 /* dkv_last_launch_count -- number of kernels the handle's last successful
- * dkv_attn_decode launched: with blocks in both pools the pool-lists kernel,
+ * attention call launched.  dkv_attn_decode: with blocks in both pools the pool-lists kernel,
  * the zero-copy host kernel, the HBM split-K kernel and the merge (4); with
- * one pool, that pool's split kernel and the merge (2). */
+ * one pool, that pool's split kernel and the merge (2).  dkv_attn_decode_window:
+ * the split kernel and the merge (2).  dkv_attn_chunk: one kernel, and a second
+ * that joins the splits where the walk over the cache was split. */
 DKV_API int dkv_last_launch_count(const dkv_handle* h, int32_t* count);
 
 /* dkv_query_plan -- the split-K decomposition of the HBM kernel of a

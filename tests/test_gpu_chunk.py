@@ -165,6 +165,69 @@ def test_many_sequences():
     once([(37 * i) % 400 for i in range(90)], [(i * 13) % 41 for i in range(90)], hkv=2, g=4, seed=8)
 
 
+# Grids that fill the GPU are not split, so that a CTA walks over many tiles.
+
+@pytest.mark.parametrize("window,sinks", [(0, 0), (300, 40), (130, 200)])
+@pytest.mark.parametrize("dtype,d", [("bf16", 128), ("f16", 128), ("bf16", 64), ("f16", 64)])
+@pytest.mark.parametrize("rows", [1, 40, 128, 140, 256, 300])
+def test_many_tiles_in_one_walk(rows, dtype, d, window, sinks):
+    # an odd and an even number of tiles, one, two and none behind the sinks
+    ctx = [1500 - rows, 1300, 130, 5, 700, 260]
+    once(ctx, [rows] * 6, hkv=32, g=1, d=d, dtype=dtype, window=window, sinks=sinks, seed=rows)
+
+
+@pytest.mark.parametrize("g", [2, 4])
+def test_many_tiles_of_shared_heads(g):
+    once([900 + 61 * i for i in range(12)], [17 + 9 * i for i in range(12)], hkv=16, g=g, s=32, seed=g)
+
+
+def test_short_chunks_on_average_with_a_long_one():
+    once([100, 0, 700, 30, 1000], [1, 2, 1, 1, 150], hkv=2, g=4, seed=20)
+    once([100, 0, 700, 30, 1000] * 8, ([1, 2, 1, 1, 150] + [1] * 5 * 7), hkv=8, g=2, seed=21)
+
+
+def test_reference_raised_in_many_tiles():
+    # scores that grow with the position: the running maximum moves in every tile, and must be followed
+    c = Chunk([1500, 1400], [128, 30], hkv=32, g=1, base=0.0, dtype="f16", seed=22)
+    for b in range(2):
+        e = len(c.cache.k[b])
+        ramp = torch.linspace(-40, 60, e)[:, None]
+        c.cache.k[b][:, :, 0] = ramp.half()
+        for j in range(-(-e // 16)):
+            bid = int(c.cache.table[b, j])
+            if bid >= 0:
+                c.cache.k_dev[bid, :, :min(16, e - 16 * j), 0] = c.cache.k[b][16 * j:16 * j + 16, :, 0].T.cuda()
+    c.q[..., 0] = 8.0
+    c.run()
+    c.verify()
+    c.free()
+
+
+def test_operands_beyond_fp16_poison_the_rows_that_see_them():
+    c = Chunk([300, 300], [20, 20], seed=23)
+    c.run()
+    good = c.out.clone()
+    bid = int(c.cache.table[1, 5])
+    c.cache.k_dev[bid, :, 3, 7] = 1e5
+    c.run()
+    assert c.attn.status() == dkv.DKV_STATUS_RANGE
+    assert torch.equal(c.out[:20], good[:20]) and c.out[20:].isnan().all()
+    c.cache.k_dev[bid, :, 3, 7] = 6e4            # the largest that is sure to fit after rotation is 65504 / sqrt(2)
+    c.cache.k_dev[bid, :, 3, 7 + 64] = 0.0
+    c.run()
+    assert c.attn.status() == 0 and torch.isfinite(c.out.float()).all()
+    # behind the last visible token anything may be stored
+    last = int(c.cache.table[1, (300 + 19) // 16])
+    c.cache.k_dev[bid, :, 3, 7] = 0.0
+    c.cache.k_dev[last, :, (300 + 19) % 16 + 1:] = 1e38
+    c.run()
+    assert c.attn.status() == 0 and torch.isfinite(c.out.float()).all()
+    c.q[25, 3, 9] = 1e6
+    c.run()
+    assert c.attn.status() == dkv.DKV_STATUS_RANGE and c.out[25, 3].isnan().all()
+    c.free()
+
+
 def test_pool_beyond_32_bit_offsets():
     # 140000 blocks of 16384 elements: K and V offsets pass 2^31 elements and 2^32 bytes
     once([200], [70], hkv=8, g=1, dev_blocks=140000, seed=9)

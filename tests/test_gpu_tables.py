@@ -292,3 +292,21 @@ def test_store_refusals():
     st.call()
     st.verify()
     st.free()
+
+
+def test_binding_refusals():
+    class KV:
+        num_kv_heads, head_dim, host_split, num_dev_blocks, batch, stride = 2, 128, 0, 4, 1, 4
+    st = Store(4)
+    bad = [(st.k_new[:, :, ::2], st.v_new, st.slots), (st.k_new.float(), st.v_new, st.slots),
+           (st.k_new, st.v_new.contiguous(), st.slots), (st.k_new, st.v_new, st.slots.int()),
+           (st.k_new, st.v_new, st.slots[:3])]
+    for k, v, slots in bad:
+        with pytest.raises(ValueError):
+            st.attn.store(k, v, slots, KV)
+    one = torch.ones(1, dtype=torch.int32, device="cuda")
+    for new, ids, count in ((one.long(), one, one), (one, one.long(), one), (one, one, one.float()),
+                            (torch.ones(2, dtype=torch.int32, device="cuda"), one, one)):
+        with pytest.raises(ValueError):
+            st.attn.extend(KV, new, ids, count, 4)
+    st.free()
