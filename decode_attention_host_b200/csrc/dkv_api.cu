@@ -33,6 +33,12 @@ int fail(int code, const std::string& msg) {
 
 int dkv::set_error(int code, const std::string& msg) { return fail(code, msg); }
 
+bool dkv::take_stall_copy() {
+  const bool armed = g_stall_copy != 0;
+  g_stall_copy = 0;
+  return armed;
+}
+
 namespace {
 
 using dkv::check_dev_pool;

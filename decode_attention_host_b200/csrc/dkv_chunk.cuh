@@ -74,6 +74,7 @@ struct ChunkParams {
   int32_t oob_host;
   int32_t window, sinks, self;
   float qscale;               // softmax scale * log2(e)
+  int32_t stall_first_copy;   // test hook: CTA 0 arms the barrier of its first key tile but issues no copy
   InvDiv div_bs, div_hkv, div_split;
 };
 
@@ -393,7 +394,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   // tokens whose rows exist: all n, unless q_start names rows outside the buffers
   const int n_rows = q0 < 0 || q0 > p.total_rows ? 0 : min(n, p.total_rows - q0);
   const bool live = m >= 0 && tok < n_rows;
-  auto place_of_row = [&] { return (static_cast<size_t>(live ? q0 + tok : 0)) * p.hq + head; };   // among all rows' heads
+  auto place_of_row = [&] { return static_cast<size_t>(live ? q0 + tok : 0) * p.hq + head; };   // of all rows' heads
 
   // this thread's row with one value: zero (an empty split), or NaN
   auto one_value = [&](bool nan) {
@@ -464,7 +465,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         const uint32_t bar = smem_u32(&full[stage]);
         if (lane == 0) mbar_arrive_expect_tx(bar, C::kTile);
         __syncwarp();
-        if (lane < nbox) {
+        if (lane < nbox && !(p.stall_first_copy && blockIdx.x == 0 && j == 0 && !is_v)) {
           const uint32_t dst = smem_u32((is_v ? sv : sk) + stage * C::kTile) + lane * box_bytes;
 #pragma unroll
           for (int x = 0; x < C::kSub; ++x) tma_load_2d(dst + x * kSubTile, host ? host_map : dev_map, 64 * x, y, bar);
@@ -873,9 +874,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         for (int i = 0; i < kC; ++i) {
           const int r = kPer * i + lane / kC, c = lane % kC;
           const int id = row_m + 32 * (warp & 3) + r, tk = id >> p.group_shift;
+          const int hd = (h << p.group_shift) + (id & ((1 << p.group_shift) - 1));
           if (tk < n_rows)
-            reinterpret_cast<uint4*>(
-                place(static_cast<size_t>(q0 + tk) * p.hq + ((h << p.group_shift) + (id & ((1 << p.group_shift) - 1)))))[c] =
+            reinterpret_cast<uint4*>(place(static_cast<size_t>(q0 + tk) * p.hq + hd))[c] =
                 *reinterpret_cast<const uint4*>(buf + r * kRow + ((c ^ (r & 7)) << 4));
         }
       };
@@ -903,7 +904,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
               uint32_t w[4];
 #pragma unroll
               for (int k = 0; k < 4; ++k)
-                w[k] = narrow2<BF16>(__uint_as_float(o[8 * e + 2 * k]) * inv, __uint_as_float(o[8 * e + 2 * k + 1]) * inv);
+                w[k] = narrow2<BF16>(__uint_as_float(o[8 * e + 2 * k]) * inv,
+                                     __uint_as_float(o[8 * e + 2 * k + 1]) * inv);
               *reinterpret_cast<uint4*>(buf + lane * (D * 2) + (((4 * i + e) ^ (lane & 7)) << 4)) =
                   make_uint4(w[0], w[1], w[2], w[3]);
             }
@@ -918,11 +920,13 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       } else if (!ok) {   // a wait ran out: copies may still be landing in shared memory
         one_value(true);
       }
-      if (ok && writes && p.nsplit == 1) flush(std::integral_constant<int, D * 2>{}, [&](size_t at) { return p.out + at * D; });
+      if (ok && writes && p.nsplit == 1)
+        flush(std::integral_constant<int, D * 2>{}, [&](size_t at) { return p.out + at * D; });
       if (ok && writes && p.nsplit > 1)
         flush(std::integral_constant<int, D * 4>{}, [&](size_t at) { return p.part_o + (at * p.nsplit + split) * D; });
       if (ok && writes && live && p.nsplit > 1)
-        p.part_lse[place_of_row() * p.nsplit + split] = nan ? __int_as_float(0x7fc00000) : (sum == 0.f ? -INFINITY : ref + __log2f(sum));
+        p.part_lse[place_of_row() * p.nsplit + split] =
+            nan ? __int_as_float(0x7fc00000) : (sum == 0.f ? -INFINITY : ref + __log2f(sum));
     }
   }
   tmem_fence_before();
@@ -974,7 +978,8 @@ __global__ void __launch_bounds__(128) chunk_merge_kernel(const ChunkParams p) {
   const float inv = nan ? __int_as_float(0x7fc00000) : (z > 0.f ? 1.f / z : 0.f);
 #pragma unroll
   for (int k = 0; k < D / 64; ++k)
-    *reinterpret_cast<uint32_t*>(p.out + w * D + 64 * k + 2 * lane) = narrow2<BF16>(acc[2 * k] * inv, acc[2 * k + 1] * inv);
+    *reinterpret_cast<uint32_t*>(p.out + w * D + 64 * k + 2 * lane) =
+        narrow2<BF16>(acc[2 * k] * inv, acc[2 * k + 1] * inv);
 }
 
 }  // namespace dkv

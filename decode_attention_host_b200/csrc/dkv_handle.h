@@ -90,7 +90,8 @@ struct dkv_handle {
   cudaStream_t aux = nullptr;
   cudaEvent_t ev_fork = nullptr;
   cudaEvent_t ev_join = nullptr;
-  dkv::SplitEntry host_kernel{}, dev_kernel{}, dev_tma_kernel{}, multi_kernel{};  // dev: cp.async; dev_tma: tensor copies
+  // dev: cp.async; dev_tma: tensor copies
+  dkv::SplitEntry host_kernel{}, dev_kernel{}, dev_tma_kernel{}, multi_kernel{};
   dkv::SplitEntry window_kernel{};
   int window_ctas = 0;         // CTAs of the windowed kernel that one wave holds
   // tensor maps of the last device pool and staging pool the HBM kernel read
@@ -139,6 +140,9 @@ inline int check_dev_pool(dkv_handle* h, const void* p, int which) {
   h->ok_dev[which] = p;
   return DKV_OK;
 }
+
+// Whether dkv_debug_stall_copy is armed on this thread; disarms it.
+bool take_stall_copy();
 
 // Picks and prepares the kernels of the serving entry points for h (dkv_serve.cu);
 // the caller has made h's device current.

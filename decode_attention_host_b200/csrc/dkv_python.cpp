@@ -112,7 +112,8 @@ PyObject* load(PyObject*, PyObject* path) {
   Py_RETURN_NONE;
 }
 
-#define DKV_FAST(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(name)), METH_FASTCALL, nullptr}
+#define DKV_FAST(name) \
+  {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(name)), METH_FASTCALL, nullptr}
 PyMethodDef g_methods[] = {DKV_FAST(extend_tables), DKV_FAST(store_kv), DKV_FAST(attn_chunk),
                            DKV_FAST(attn_decode_window), {"load", load, METH_O, nullptr},
                            {nullptr, nullptr, 0, nullptr}};

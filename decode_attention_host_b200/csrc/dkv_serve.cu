@@ -43,8 +43,9 @@ dkv::SplitEntry window_entry() {
 template <int D, bool BF16, bool ROPE>
 cudaError_t launch_chunk(cudaStream_t s, const dkv::ChunkParams& p, const dkv::ChunkMaps& m, int ctas,
                          int rows) {
-  if (rows == 128) dkv::chunk_kernel<D, BF16, ROPE, true><<<ctas, dkv::kChunkThreads, dkv::chunk_smem_bytes<D>(), s>>>(p, m);
-  else dkv::chunk_kernel<D, BF16, ROPE, false><<<ctas, dkv::kChunkThreads, dkv::chunk_smem_bytes<D>(), s>>>(p, m);
+  constexpr size_t kSmem = dkv::chunk_smem_bytes<D>();
+  if (rows == 128) dkv::chunk_kernel<D, BF16, ROPE, true><<<ctas, dkv::kChunkThreads, kSmem, s>>>(p, m);
+  else dkv::chunk_kernel<D, BF16, ROPE, false><<<ctas, dkv::kChunkThreads, kSmem, s>>>(p, m);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || p.nsplit == 1) return e;
   cudaLaunchConfig_t cfg{};
@@ -198,7 +199,8 @@ int dkv_extend_tables(dkv_handle* h, const int32_t* seq_lens, const int32_t* new
                       int64_t* slot_map, int32_t max_slots, dkv_stream_t stream) {
   if (!h) return set_error(DKV_ERR_INVALID_ARG, "dkv_extend_tables: null handle");
   const dkv_config& c = h->cfg;
-  if (batch < 1 || batch > c.max_batch) return set_error(DKV_ERR_INVALID_ARG, "dkv_extend_tables: batch outside [1, max_batch]");
+  if (batch < 1 || batch > c.max_batch)
+    return set_error(DKV_ERR_INVALID_ARG, "dkv_extend_tables: batch outside [1, max_batch]");
   if (batch > dkv::kTableMaxBatch) return set_error(DKV_ERR_UNSUPPORTED, "dkv_extend_tables: batch above 8192");
   if (!seq_lens || !new_lens || !block_table || !free_count || !free_left || !q_start ||
       (!free_ids && free_capacity > 0) || (!slot_map && max_slots > 0))
@@ -206,7 +208,8 @@ int dkv_extend_tables(dkv_handle* h, const int32_t* seq_lens, const int32_t* new
   if (block_table_stride < 1 || free_capacity < 0 || free_capacity > (1 << 30) || max_slots < 0 ||
       max_slots > (1 << 30))
     return set_error(DKV_ERR_INVALID_ARG, "dkv_extend_tables: stride, free_capacity or max_slots out of range");
-  if (misaligned(slot_map, 8)) return set_error(DKV_ERR_INVALID_ARG, "dkv_extend_tables: slot_map must be 8-byte aligned");
+  if (misaligned(slot_map, 8))
+    return set_error(DKV_ERR_INVALID_ARG, "dkv_extend_tables: slot_map must be 8-byte aligned");
   dkv::DeviceGuard guard(c.device);
   if (!guard.ok) return set_error(DKV_ERR_CUDA, "cudaSetDevice failed");
   dkv::TableParams p{};
@@ -230,7 +233,8 @@ int dkv_extend_tables(dkv_handle* h, const int32_t* seq_lens, const int32_t* new
   p.wide = !misaligned(slot_map, 16);
   // a run of slots per thread, up to one wave
   constexpr long long kRun = dkv::kTableRun * dkv::kTableThreads;
-  const long long want = (static_cast<long long>(max_slots) + kRun - 1) / kRun, wave = dkv::kTableCtasPerSm * h->sm_count;
+  const long long want = (static_cast<long long>(max_slots) + kRun - 1) / kRun;
+  const long long wave = dkv::kTableCtasPerSm * h->sm_count;
   const int ctas = static_cast<int>(want < 1 ? 1 : want > wave ? wave : want);
   dkv::extend_tables_kernel<<<ctas, dkv::kTableThreads, dkv::table_smem_bytes(batch),
                               reinterpret_cast<cudaStream_t>(stream)>>>(p);
@@ -289,7 +293,8 @@ int dkv_attn_chunk(dkv_handle* h, const void* q, int64_t q_stride, const int32_t
                    int32_t block_table_stride, int32_t num_dev_blocks, void* k_stage, void* v_stage) {
   if (!h) return set_error(DKV_ERR_INVALID_ARG, "dkv_attn_chunk: null handle");
   const dkv_config& c = h->cfg;
-  if (batch < 0 || batch > c.max_batch) return set_error(DKV_ERR_INVALID_ARG, "dkv_attn_chunk: batch outside [0, max_batch]");
+  if (batch < 0 || batch > c.max_batch)
+    return set_error(DKV_ERR_INVALID_ARG, "dkv_attn_chunk: batch outside [0, max_batch]");
   if (total_rows < 0 || total_rows > (1 << 28))
     return set_error(DKV_ERR_INVALID_ARG, "dkv_attn_chunk: total_rows outside [0, 2^28]");
   int rc = check_mask("dkv_attn_chunk", window, sinks, include_self, 0);
@@ -351,6 +356,7 @@ int dkv_attn_chunk(dkv_handle* h, const void* q, int64_t q_stride, const int32_t
   p.sinks = window ? sinks : 0;
   p.self = include_self;
   p.qscale = h->qscale;
+  p.stall_first_copy = dkv::take_stall_copy() ? 1 : 0;
   // 128 rows to a CTA while a sequence has no more of them on average (a kv head's rows: its tokens times G)
   const int rows = static_cast<long long>(total_rows) * h->G <= 128LL * batch ? 128 : 256;
   // sum over b of ceil(rows_b G / rows), rows_b unknown here, is at most this
@@ -389,7 +395,8 @@ int dkv_attn_chunk(dkv_handle* h, const void* q, int64_t q_stride, const int32_t
     if (code == 0) code = dkv::encode_box_map(&maps.v_host, v_host, host_rows, D, p.box);
   }
   if (code != 0)
-    return set_error(DKV_ERR_CUDA, "cuTensorMapEncodeTiled rejected the pool's tensor map (" + std::to_string(code) + ")");
+    return set_error(DKV_ERR_CUDA,
+                     "cuTensorMapEncodeTiled rejected the pool's tensor map (" + std::to_string(code) + ")");
   DKV_CUDA(by_shape(c, LaunchChunk{s, p, maps, static_cast<int>(units * p.nsplit), rows}));
   h->last_launches = p.nsplit > 1 ? 2 : 1;
   return DKV_OK;

@@ -406,7 +406,9 @@ DKV_API int dkv_debug_fail_alloc(int32_t nth);
  * barrier of the unit's first tile copy but issues no copy, so its bounded
  * wait runs out (about 2 s): the call must then report
  * DKV_STATUS_COPY_TIMEOUT, write NaN for that warp's units and leave the
- * device usable.  The hook is
+ * device usable.  A dkv_attn_chunk that comes first takes the hook instead:
+ * its first CTA leaves its first key tile uncopied, and the rows of that CTA
+ * become NaN.  The hook is
  * cleared by that call; 0 disarms it.  Always returns DKV_OK. */
 DKV_API int dkv_debug_stall_copy(int32_t enable);
 

@@ -324,6 +324,24 @@ def test_nan_key_reaches_the_rows_that_see_it():
     c.free()
 
 
+@pytest.mark.parametrize("new", [[130, 20], [9, 3]])
+def test_a_copy_that_never_completes_times_out_and_is_reported(new):
+    """Every wait is bounded: a key tile that never lands (the hook arms its barrier and issues no copy) ends the
+    waits of its CTA after about 2 s each, with NaN rows there; the other rows and the next call are clean."""
+    c = Chunk([1500, 600], new, hkv=40, g=4, seed=24)      # more units than SMs: the walk is not split
+    c.run()
+    good = c.out.clone()
+    dkv.dkv_debug_stall_copy(True)
+    c.run()
+    assert c.attn.status() == dkv.DKV_STATUS_COPY_TIMEOUT
+    bad = c.out.isnan().any(-1)
+    assert bad.any() and not bad.all()
+    assert torch.equal(c.out[~bad], good[~bad])
+    c.run()
+    assert c.attn.status() == 0 and torch.equal(c.out, good)
+    c.free()
+
+
 def test_refusals():
     c = Chunk([20], [8], seed=18)
     a, k = c.attn, c.cache
