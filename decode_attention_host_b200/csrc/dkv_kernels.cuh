@@ -705,6 +705,10 @@ __global__ void __launch_bounds__(kThreads) split_kernel(const SplitParams p, co
   static_assert(G >= 1 && G <= 4, "query group of 1, 2 or 4 heads");
   static_assert(NST <= 4, "SplitSmemTail is sized for up to 4 stages");
   static_assert(!(WIN && TMA), "windowed launches read both pools with cp.async");
+  // Windowed launches split a weight into three bf16 parts (2^-24; two leave
+  // 2^-17, most of the output's error): the third takes the rows 8..11 that the
+  // PV mma has to spare.  fp16's two parts reach 2^-22.
+  constexpr bool kThree = WIN && BF16;
   constexpr int PPL = D / 16;                  // NeoX pairs per lane
   constexpr int NP2 = PPL / 2;                 // fp32 pairs per half-row per lane
   constexpr int ROW = D * 2;                   // bytes of one token row
@@ -875,7 +879,7 @@ __global__ void __launch_bounds__(kThreads) split_kernel(const SplitParams p, co
   // bf16/fp16 "hi" part of the weights (lanes 0..4G-1), rows 4..4+G-1 the "lo"
   // remainder (lanes 16..16+4G-1); out = row g + row 4+g.
   float2 QX[G][NP2], QY[G][NP2];
-  float acc[NT][2];
+  float acc[NT][kThree ? 4 : 2];
   // After the reduce-scatter of the scores, lane li of every token group owns
   // head gl of the softmax (G=4: gl = li/2; G=2: li/4; G=1: 0) and keeps that
   // head's running max and (lane-partial) running sum.
@@ -918,7 +922,10 @@ __global__ void __launch_bounds__(kThreads) split_kernel(const SplitParams p, co
     mrun = -1e30f;
     lrun = 0.f;
 #pragma unroll
-    for (int n = 0; n < NT; ++n) acc[n][0] = acc[n][1] = 0.f;
+    for (int n = 0; n < NT; ++n) {
+      acc[n][0] = acc[n][1] = 0.f;
+      if constexpr (kThree) acc[n][2] = acc[n][3] = 0.f;
+    }
     poisoned = false;
   };
 
@@ -946,6 +953,10 @@ __global__ void __launch_bounds__(kThreads) split_kernel(const SplitParams p, co
     // hi rows (lanes 0..15) + lo rows (lanes 16..31) of the same head and columns
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
+      if constexpr (kThree) {
+        acc[n][0] += acc[n][2];
+        acc[n][1] += acc[n][3];
+      }
       acc[n][0] += __shfl_xor_sync(kFull, acc[n][0], 16);
       acc[n][1] += __shfl_xor_sync(kFull, acc[n][1], 16);
     }
@@ -1045,6 +1056,10 @@ __global__ void __launch_bounds__(kThreads) split_kernel(const SplitParams p, co
       for (int n = 0; n < NT; ++n) {
         acc[n][0] *= al;
         acc[n][1] *= al;
+        if constexpr (kThree) {
+          acc[n][2] *= al;
+          acc[n][3] *= al;
+        }
       }
     }
     float psum = 0.f;
@@ -1066,7 +1081,7 @@ __global__ void __launch_bounds__(kThreads) split_kernel(const SplitParams p, co
     __syncwarp();
     // ---- PV on the tensor cores.  A rows 0..7 (lane >> 2): rows 0..3 hi,
     // rows 4..7 lo, of head (lane >> 2) & 3; B = V from the swizzled tile.
-    uint32_t a[2] = {0u, 0u};
+    uint32_t a[2] = {0u, 0u}, a3[2] = {0u, 0u};
     const int gA = gT & 3;
     if (gA < G) {
       // tokens 2c, 2c+1 (a[0]) and 2c+8, 2c+9 (a[1]); token t lives at [t % 4][t / 4]
@@ -1077,6 +1092,13 @@ __global__ void __launch_bounds__(kThreads) split_kernel(const SplitParams p, co
       uint32_t ha, la, hb, lb;
       split_hi_lo<BF16>(pa, ha, la);
       split_hi_lo<BF16>(pb, hb, lb);
+      if constexpr (kThree) {
+        const float2 fa = widen2<true>(ha), ga = widen2<true>(la), fb = widen2<true>(hb), gb = widen2<true>(lb);
+        const __nv_bfloat162 ra = __floats2bfloat162_rn(pa.x - fa.x - ga.x, pa.y - fa.y - ga.y);
+        const __nv_bfloat162 rb = __floats2bfloat162_rn(pb.x - fb.x - gb.x, pb.y - fb.y - gb.y);
+        a3[0] = lane < 16 ? *reinterpret_cast<const uint32_t*>(&ra) : 0u;
+        a3[1] = lane < 16 ? *reinterpret_cast<const uint32_t*>(&rb) : 0u;
+      }
       a[0] = lane < 16 ? ha : la;
       a[1] = lane < 16 ? hb : lb;
     }
@@ -1084,8 +1106,14 @@ __global__ void __launch_bounds__(kThreads) split_kernel(const SplitParams p, co
     for (int qd = 0; qd < D / 16; ++qd) {
       uint32_t b0, b1, b2, b3;
       ldsm_x4_t(sv + vofs_q[qd & 3] + (qd >> 2) * (kTileTokens * 128), b0, b1, b2, b3);
-      mma16816_top<BF16>(acc[2 * qd], a, b0, b1);
-      mma16816_top<BF16>(acc[2 * qd + 1], a, b2, b3);
+      if constexpr (kThree) {
+        const uint32_t all[4] = {a[0], a3[0], a[1], a3[1]};
+        mma16816_full<BF16>(acc[2 * qd], all, b0, b1);
+        mma16816_full<BF16>(acc[2 * qd + 1], all, b2, b3);
+      } else {
+        mma16816_top<BF16>(acc[2 * qd], a, b0, b1);
+        mma16816_top<BF16>(acc[2 * qd + 1], a, b2, b3);
+      }
     }
   };
 
