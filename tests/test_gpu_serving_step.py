@@ -112,6 +112,38 @@ def test_steps_as_one_captured_graph(window, sinks):
         e.verify()
 
 
+def test_first_calls_of_a_handle_inside_a_capture():
+    e = Engine(100, 5, host_blocks=20)
+    e.draw(STEPS[0])
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        e.step()
+    g.replay()
+    e.verify()
+    for new in STEPS[1:]:
+        e.draw(new)
+        g.replay()
+        e.verify()
+
+
+def test_two_graphs_of_one_handle_replayed_in_turn():
+    e = Engine(100, 5)
+    graphs = []
+    for new in STEPS[:2]:
+        e.draw(new)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            e.step()
+        g.replay()
+        e.verify()
+        graphs.append(g)
+    for i, new in enumerate(STEPS[2:]):
+        e.draw(new)
+        graphs[i % 2].replay()
+        e.verify()
+
+
 def test_two_handles_on_two_streams():
     es = [Engine(100, 5), Engine(0, 0, dtype="f16")]
     streams = [torch.cuda.Stream() for _ in es]

@@ -57,3 +57,41 @@ int main() {
             assert diff <= Fraction(pos + 1, 2 ** 62), (f, pos)
             seen += 1
     assert seen == 6 * (32 + 64) * 3 and math.isclose(float(two_pi), 2 * math.pi)
+
+
+def test_even_split_plan_covers_every_block_and_stays_in_the_workspace(tmp_path):
+    """plan_split_even on a grid of sizes: every block in some split, no split empty, never fewer splits than the
+    plain plan and never more than 16 beyond it or max_nsplit, and no costlier plan than the plain one."""
+    src = tmp_path / "plan.cpp"
+    src.write_text(r"""
+#include <cstdio>
+#include <initializer_list>
+#include "dkv_plan.h"
+int main() {
+  long n = 0;
+  for (int bs : {16, 48, 256, 1024})
+    for (int nblk : {1, 2, 3, 17, 66, 259, 2048, 65536})
+      for (long per : {1L, 3L, 8L, 512L, 2048L, 100000L})
+        for (long warps : {1184L, 1776L, 4736L})
+          for (long cap : {1L, 7L, 40L, 100000L}) {
+            const dkv::SplitPlan a = dkv::plan_split(nblk, per, bs, warps, 0);
+            const dkv::SplitPlan b = dkv::plan_split_even(nblk, per, bs, warps, cap);
+            auto cost = [&](const dkv::SplitPlan& s) {
+              return static_cast<double>((per * s.nsplit + warps - 1) / warps) * (static_cast<double>(s.bps) * bs + 48);
+            };
+            if (static_cast<long>(b.nsplit) * b.bps < nblk || static_cast<long>(b.nsplit - 1) * b.bps >= nblk) return 1;
+            if (b.nsplit < a.nsplit || b.nsplit > a.nsplit + 16) return 2;
+            if (b.nsplit > a.nsplit && b.nsplit > cap) return 3;
+            if (cost(b) > cost(a)) return 4;
+            ++n;
+          }
+  printf("%ld\n", n);
+  // 64 sequences of 8 kv heads, 259 visible blocks of 16: four nearly full rounds of 9 splits
+  return dkv::plan_split_even(259, 512, 16, 1184, 1 << 20).nsplit == 9 ? 0 : 5;
+}
+""")
+    exe = tmp_path / "plan"
+    subprocess.run(["g++", "-std=c++17", f"-I{ROOT}/decode_attention_host_b200/csrc", "-o", str(exe), str(src)],
+                   check=True)
+    r = subprocess.run([str(exe)], capture_output=True, text=True)
+    assert r.returncode == 0, r.returncode
