@@ -516,6 +516,25 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         for (int i = 0; i < kChunkTokens / 16; ++i)
           umma_ts(tm + 256 + D * g, tm + 128 * g + 8 * i, v + i * (2048 >> 4), kIdPV, acc || i > 0, on);
       };
+      // V rows that no row of the CTA sees hold anything: their weights are 0, but
+      // 0 * NaN is not, so they are zeroed.  Here, as this warp waits for every use
+      // of V's stages in turn; the rotating warps, which run ahead, cannot tell a
+      // stage's use from the one two before it by the barrier's parity.
+      auto clear_unseen = [&](int j, int stage) {
+        const int p0 = tile_pos(j);
+        if (p0 + kChunkTokens <= hi_max && (p0 >= lo_min || p0 + kChunkTokens <= sk_end)) return;
+#pragma unroll 1
+        for (int r = lane; r < kChunkTokens; r += 32) {
+          const int tt = p0 + r;
+          if (tt < hi_max && (tt >= lo_min || tt < sk_end)) continue;
+          char* const v = sv + stage * C::kTile + r * 128;
+#pragma unroll
+          for (int e = 0; e < 8 * C::kSub; ++e)
+            *reinterpret_cast<uint4*>(v + (e >> 3) * kSubTile + (e & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+        }
+        fence_proxy_async();
+        __syncwarp();
+      };
       Ring rk, rv;
       bool ok = chunk_wait(&t.q_ready[0], 0, t, p.status);
       const int row_tiles = __shfl_sync(kFull, rows > 128 ? 2 : 1, 0);
@@ -534,6 +553,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         for (int j = 0; j < tiles; ++j) {
           const bool more = j + 1 < tiles;
           ok = __all_sync(kFull, chunk_wait(&t.v_full[rv.stage], rv.parity, t, p.status));
+          if (ok) clear_unseen(j, rv.stage);
 #pragma unroll 1   // unrolled, its operands no longer fit in uniform registers: 4% slower
           for (int g = 0; g < row_tiles && ok; ++g) {
             ok = chunk_wait(&t.p_ready[g], j & 1, t, p.status);
@@ -568,6 +588,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
           ok = chunk_wait(&t.v_full[rv.stage], rv.parity, t, p.status);
           ok = ok && chunk_wait(&t.p_ready[j & 1], (j >> 1) & 1, t, p.status);
           if (!(ok = __all_sync(kFull, ok))) break;
+          clear_unseen(j, rv.stage);
           tmem_fence_after();
           pv(j & 1, v_low + rv.stage * (C::kTile >> 4), j > 1);
           umma_commit(smem_u32(&t.v_free[rv.stage]), on);
@@ -601,7 +622,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       }
     }
     int next_pos = -1, chain = 0;
-    Ring rk, rv;
+    Ring rk;
     for (int j = 0; j < nt; ++j) {
       const int p0 = tile_pos(j);
       const bool edge = p0 + kChunkTokens > hi_max || (p0 < lo_min && p0 + kChunkTokens > sk_end);
@@ -654,22 +675,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
           atomicOr(p.status, kStatusRange);
         }
       }
-      if (edge) {
-        // V rows that no row sees: their weights are 0, but 0 * NaN is not
-        if (!__all_sync(kFull, chunk_wait(&t.v_full[rv.stage], rv.parity, t, p.status))) break;
-        const int tt = p0 + r;
-        if (tt >= hi_max || (tt < lo_min && tt >= sk_end)) {
-          char* const v = sv + rv.stage * C::kTile + r * 128;
-#pragma unroll
-          for (int e = 0; e < 8 * C::kSub; ++e)
-            *reinterpret_cast<uint4*>(v + (e >> 3) * kSubTile + (e & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
-        }
-      }
       fence_proxy_async();   // the products read what was written here
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&t.k_ready[rk.stage]));
       rk.next<C::kStagesK>();
-      rv.next<kStagesV>();
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));

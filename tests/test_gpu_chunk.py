@@ -176,6 +176,19 @@ def test_many_tiles_in_one_walk(rows, dtype, d, window, sinks):
     once(ctx, [rows] * 6, hkv=32, g=1, d=d, dtype=dtype, window=window, sinks=sinks, seed=rows)
 
 
+@pytest.mark.parametrize("window,sinks", [(0, 0), (300, 40)])
+@pytest.mark.parametrize("dtype,d,s", [("bf16", 128, 16), ("f16", 128, 64), ("bf16", 64, 32), ("f16", 64, 128)])
+@pytest.mark.parametrize("new", [256, 257, 300, 384, 385, 512])
+def test_long_chunks(new, dtype, d, s, window, sinks):
+    # 4 to 8 row tiles of 256 rows, an even and an odd number, full and ragged ends; walks whole and split
+    once([700, 0, 33], [new] * 3, hkv=16, g=4, d=d, s=s, dtype=dtype, window=window, sinks=sinks, seed=new)
+    once([1000], [new], hkv=1, g=4, d=d, s=s, dtype=dtype, window=window, sinks=sinks, self_=0, seed=new + 1)
+
+
+def test_long_chunks_with_short_and_empty_ones():
+    once([0, 64, 1000, 3], [900, 0, 1, 700], hkv=8, g=4, host=0.2, seed=30, pad=3)
+
+
 @pytest.mark.parametrize("g", [2, 4])
 def test_many_tiles_of_shared_heads(g):
     once([900 + 61 * i for i in range(12)], [17 + 9 * i for i in range(12)], hkv=16, g=g, s=32, seed=g)
@@ -324,7 +337,7 @@ def test_nan_key_reaches_the_rows_that_see_it():
     c.free()
 
 
-@pytest.mark.parametrize("new", [[130, 20], [9, 3]])
+@pytest.mark.parametrize("new", [[130, 20], [9, 3], [400, 300]])
 def test_a_copy_that_never_completes_times_out_and_is_reported(new):
     """Every wait is bounded: a key tile that never lands (the hook arms its barrier and issues no copy) ends the
     waits of its CTA after about 2 s each, with NaN rows there; the other rows and the next call are clean."""
