@@ -26,6 +26,15 @@
 //               value leaves its thread, the running maximum is raised lazily
 //               (only past 2^8, so O is rescaled rarely), P goes back to TMEM
 //               over the S it came from
+// A chunk of at most 128 rows a kv head takes CTAs of 128 rows (DUAL, below).
+//
+// Measured on a B200, 32 query heads over 8 kv heads, D = 128, bf16: 2048 rows on
+// 30720 tokens in 1.08 ms, 0.99 PFLOP/s (0.6 of a plain matrix product; without
+// rotation 0.89 ms, 1.2 PFLOP/s); 8 rows on four 64k contexts in 202 us, 5.3 TB/s.
+// A K/V tile takes about 3900 cycles where its products take 2100: the softmax
+// warps and the rotating one share the schedulers, 47% of whose slots issue, and
+// the tensor core waits for P.  The 128 x 128 tiles are what TMEM's 512 columns
+// hold twice (S and O); N = 64 halves the products' rate.
 //
 // Roundings to 16 bits: rotated queries and keys are held in fp16 for both
 // cache types (fp32 rotation, one rounding to 2^-11; bf16 operands would be
