@@ -13,6 +13,7 @@ only bundle those calls for the tests and the benchmark.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from pathlib import Path
@@ -441,7 +442,8 @@ class DecodeAttention:
 
     def extend(self, kv: PagedKV, new_lens, free_ids, free_count, max_slots: int, stream=None):
         """Blocks and slots for new_lens[b] more tokens of every sequence (device int32 tensors): returns
-        (q_start, slot_map); kv's table grows and free_count goes down in place, kv.seq_lens_dev stays."""
+        (q_start, slot_map); kv's table grows and free_count goes down in place, kv.seq_lens_dev stays.  Both are
+        memory of the stream the call runs on: another stream that uses them waits for it and records its use."""
         import torch
         dev = new_lens.device
         for x in (new_lens, free_ids, free_count):
@@ -449,10 +451,12 @@ class DecodeAttention:
                 raise ValueError("new_lens, free_ids and free_count are contiguous int32 tensors")
         if new_lens.numel() != kv.batch or free_count.numel() != 1:
             raise ValueError("new_lens holds one length for each sequence, free_count one number")
+        on_stream = contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
         if stream is None:
             stream = torch.cuda.current_stream(dev)
-        q_start = torch.empty(kv.batch + 1, dtype=torch.int32, device=dev)
-        slot_map = torch.empty(max_slots, dtype=torch.int64, device=dev)
+        with on_stream:   # memory of the current stream could still be in use by what is queued there
+            q_start = torch.empty(kv.batch + 1, dtype=torch.int32, device=dev)
+            slot_map = torch.empty(max_slots, dtype=torch.int64, device=dev)
         dkv_extend_tables(self.handle, kv.seq_lens_dev, new_lens, kv.batch, kv.table_dev, kv.stride, free_ids,
                           free_ids.numel(), free_count, free_count, q_start, slot_map, max_slots, stream.cuda_stream)
         return q_start, slot_map
