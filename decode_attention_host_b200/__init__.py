@@ -400,6 +400,22 @@ class DecodeAttention:
                              float(scale), max_batch, max_blocks_per_seq, device, host_ctas)
         self.handle = dkv_create(self.cfg)
 
+    def _check_cache(self, kv) -> None:
+        """The serving step's calls address the pools by the handle's shape."""
+        c = self.cfg
+        if (kv.num_kv_heads, kv.head_dim, getattr(kv, "block_size", c.block_size)) != \
+                (c.num_kv_heads, c.head_dim, c.block_size):
+            raise ValueError("the cache has other kv heads, head dim or block size than the handle")
+
+    def _check_device(self, **tensors) -> None:
+        for name, x in tensors.items():
+            if not x.is_cuda or x.get_device() != self.cfg.device:
+                raise ValueError(f"{name} must be on GPU {self.cfg.device}, the handle's")
+
+    def _kv_type(self):
+        import torch
+        return torch.bfloat16 if self.cfg.kv_dtype == DKV_KV_BF16 else torch.float16
+
     def __call__(self, q, kv: PagedKV, out, stream=None) -> None:
         """out[B, Hq, D] = decode attention of q[B, Hq, D] over the cache ``kv`` (async on ``stream``)."""
         import torch
@@ -451,6 +467,9 @@ class DecodeAttention:
                 raise ValueError("new_lens, free_ids and free_count are contiguous int32 tensors")
         if new_lens.numel() != kv.batch or free_count.numel() != 1:
             raise ValueError("new_lens holds one length for each sequence, free_count one number")
+        self._check_cache(kv)
+        self._check_device(new_lens=new_lens, free_ids=free_ids, free_count=free_count, table_dev=kv.table_dev,
+                           seq_lens_dev=kv.seq_lens_dev)
         on_stream = contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
         if stream is None:
             stream = torch.cuda.current_stream(dev)
@@ -462,18 +481,21 @@ class DecodeAttention:
         return q_start, slot_map
 
     def store(self, k_new, v_new, slot_map, kv: PagedKV, stream=None) -> None:
-        """Store k_new, v_new [rows, Hkv, D] (16-bit; rows may be strided, elements of a row are not) at slot_map."""
+        """Store k_new, v_new [rows, Hkv, D] (of the handle's type; rows may be strided, elements of a row are not) at
+        slot_map."""
         import torch
+        self._check_cache(kv)
         rows = k_new.shape[0]
         width = kv.num_kv_heads * kv.head_dim
         for x in (k_new, v_new):
-            if x.shape != (rows, kv.num_kv_heads, kv.head_dim) or x.element_size() != 2 or \
+            if x.shape != (rows, kv.num_kv_heads, kv.head_dim) or x.dtype != self._kv_type() or \
                     (rows and x.stride()[1:] != (kv.head_dim, 1)):
-                raise ValueError("k_new and v_new are 16-bit [rows, Hkv, D] with contiguous rows")
+                raise ValueError(f"k_new and v_new are {self._kv_type()} [rows, Hkv, D] with contiguous rows")
         if rows > 1 and k_new.stride(0) != v_new.stride(0):
             raise ValueError("k_new and v_new have one row stride")
         if slot_map.dtype != torch.int64 or not slot_map.is_contiguous() or slot_map.numel() < rows:
             raise ValueError("slot_map is contiguous int64 with a slot for every row")
+        self._check_device(k_new=k_new, v_new=v_new, slot_map=slot_map)
         if stream is None:
             stream = torch.cuda.current_stream(k_new.device)
         dkv_store_kv(self.handle, k_new, v_new, k_new.stride(0) if rows > 1 else width, slot_map, rows, kv.host_split,
@@ -482,16 +504,24 @@ class DecodeAttention:
 
     def chunk(self, q, q_start, kv: PagedKV, out, window: int = 0, sinks: int = 0, include_self: bool = True,
               k_stage=None, v_stage=None, stream=None) -> None:
-        """q, out [rows, Hq, D] (16-bit): rows q_start[b] .. q_start[b+1] are the new tokens of sequence b, at
-        positions seq_lens[b] ..; causal over the cache, under a window of tokens and sinks if window > 0."""
+        """q, out [rows, Hq, D] (of the handle's type): rows q_start[b] .. q_start[b+1] are the new tokens of sequence b,
+        at positions seq_lens[b] ..; causal over the cache, under a window of tokens and sinks if window > 0."""
         import torch
         hq, d = self.cfg.num_q_heads, self.cfg.head_dim
         rows = q.shape[0]
-        if q.shape[1:] != (hq, d) or q.element_size() != 2 or (rows and q.stride()[1:] != (d, 1)) or \
+        self._check_cache(kv)
+        if q.shape[1:] != (hq, d) or q.dtype != self._kv_type() or (rows and q.stride()[1:] != (d, 1)) or \
                 out.shape != q.shape or out.dtype != q.dtype or not out.is_contiguous():
-            raise ValueError("q is 16-bit [rows, Hq, D] with contiguous rows, out the same and contiguous")
+            raise ValueError(f"q is {self._kv_type()} [rows, Hq, D] with contiguous rows, out the same and contiguous")
         if q_start.dtype != torch.int32 or not q_start.is_contiguous() or q_start.numel() != kv.batch + 1:
             raise ValueError("q_start is contiguous int32 [batch + 1]")
+        if k_stage is not None or v_stage is not None:
+            need = 2 * kv.host_split * kv.num_kv_heads * self.cfg.block_size * d
+            for x in (k_stage, v_stage):
+                if x is None or not x.is_contiguous() or x.numel() * x.element_size() < need:
+                    raise ValueError("k_stage and v_stage are contiguous and hold the blocks of the host pools")
+            self._check_device(k_stage=k_stage, v_stage=v_stage)
+        self._check_device(q=q, q_start=q_start, out=out, table_dev=kv.table_dev, seq_lens_dev=kv.seq_lens_dev)
         if stream is None:
             stream = torch.cuda.current_stream(q.device)
         dkv_attn_chunk(self.handle, q, q.stride(0) if rows > 1 else hq * d, q_start, rows, kv.k_host.ptr or None,
@@ -504,6 +534,12 @@ class DecodeAttention:
                stream=None) -> None:
         """q, out [B, Hq, D] fp32: decode attention over the last `window` tokens and the first `sinks`."""
         import torch
+        self._check_cache(kv)
+        for x in (q, out):
+            if x.dtype != torch.float32 or x.shape != (kv.batch, self.cfg.num_q_heads, self.cfg.head_dim) or \
+                    not x.is_contiguous():
+                raise ValueError("q and out are contiguous float32 [batch, Hq, D]")
+        self._check_device(q=q, out=out, table_dev=kv.table_dev, seq_lens_dev=kv.seq_lens_dev)
         if stream is None:
             stream = torch.cuda.current_stream(q.device)
         dkv_attn_decode_window(self.handle, window, sinks, include_self, q, kv.k_host.ptr or None,
