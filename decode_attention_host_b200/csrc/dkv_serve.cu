@@ -319,14 +319,10 @@ int dkv_attn_chunk(dkv_handle* h, const void* q, int64_t q_stride, const int32_t
   if ((rc = check_cache(h, "dkv_attn_chunk", k_host, v_host, k_dev, v_dev, host_split, num_dev_blocks)) != DKV_OK)
     return rc;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (staged && host_split > 0) {
+  const bool copies = staged && host_split > 0;
+  if (copies) {
     if ((rc = dkv::check_dev_pool(h, k_stage, 2)) != DKV_OK) return rc;
     if ((rc = dkv::check_dev_pool(h, v_stage, 3)) != DKV_OK) return rc;
-    const size_t bytes = static_cast<size_t>(host_split) * c.num_kv_heads * c.block_size * c.head_dim * 2;
-    DKV_CUDA(cudaMemcpyAsync(k_stage, k_host, bytes, cudaMemcpyHostToDevice, s));
-    DKV_CUDA(cudaMemcpyAsync(v_stage, v_host, bytes, cudaMemcpyHostToDevice, s));
-    k_host = k_stage;
-    v_host = v_stage;
   }
   dkv::ChunkParams p{};
   p.q = static_cast<const uint16_t*>(q);
@@ -356,7 +352,6 @@ int dkv_attn_chunk(dkv_handle* h, const void* q, int64_t q_stride, const int32_t
   p.sinks = window ? sinks : 0;
   p.self = include_self;
   p.qscale = h->qscale;
-  p.stall_first_copy = dkv::take_stall_copy() ? 1 : 0;
   // 128 rows to a CTA while a sequence has no more of them on average (a kv head's rows: its tokens times G)
   const int rows = static_cast<long long>(total_rows) * h->G <= 128LL * batch ? 128 : 256;
   // sum over b of ceil(rows_b G / rows), rows_b unknown here, is at most this
@@ -391,12 +386,19 @@ int dkv_attn_chunk(dkv_handle* h, const void* q, int64_t q_stride, const int32_t
     if (code == 0) code = dkv::encode_box_map(&maps.v_dev, v_dev, dev_rows, D, p.box);
   }
   if (code == 0 && host_rows) {
-    code = dkv::encode_box_map(&maps.k_host, k_host, host_rows, D, p.box);
-    if (code == 0) code = dkv::encode_box_map(&maps.v_host, v_host, host_rows, D, p.box);
+    code = dkv::encode_box_map(&maps.k_host, copies ? k_stage : k_host, host_rows, D, p.box);
+    if (code == 0) code = dkv::encode_box_map(&maps.v_host, copies ? v_stage : v_host, host_rows, D, p.box);
   }
   if (code != 0)
     return set_error(DKV_ERR_CUDA,
                      "cuTensorMapEncodeTiled rejected the pool's tensor map (" + std::to_string(code) + ")");
+  // from here on nothing refuses the call: only now is anything put on the stream, or the test hook taken
+  if (copies) {
+    const size_t bytes = static_cast<size_t>(host_rows) * D * 2;
+    DKV_CUDA(cudaMemcpyAsync(k_stage, k_host, bytes, cudaMemcpyHostToDevice, s));
+    DKV_CUDA(cudaMemcpyAsync(v_stage, v_host, bytes, cudaMemcpyHostToDevice, s));
+  }
+  p.stall_first_copy = dkv::take_stall_copy() ? 1 : 0;
   DKV_CUDA(by_shape(c, LaunchChunk{s, p, maps, static_cast<int>(units * p.nsplit), rows}));
   h->last_launches = p.nsplit > 1 ? 2 : 1;
   return DKV_OK;
