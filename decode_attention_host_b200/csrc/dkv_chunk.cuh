@@ -24,8 +24,8 @@
 //               tile that is rotated once serves 256 rows
 //   warps 8-11, 12-15  the softmax of row tile 0 and 1, a thread per row: no
 //               value leaves its thread, the running maximum is raised lazily
-//               (only past 2^8, so O is rescaled rarely), P goes back to TMEM
-//               over the S it came from
+//               (only past 2^8, or 2^4 with fp16 weights, so O is rescaled
+//               rarely), P goes back to TMEM over the S it came from
 // A chunk of at most 128 rows a kv head takes CTAs of 128 rows (DUAL, below).
 //
 // Measured on a B200, 32 query heads over 8 kv heads, D = 128, bf16: 2048 rows on
@@ -62,6 +62,15 @@ constexpr int kRegsRotate = 96;
 constexpr int kRegsSoftmax = 176;
 static_assert(kRegsIssue + kRegsRotate + 2 * kRegsSoftmax <= 4 * kRegsLaunch, "setmaxnreg.inc would wait for ever");
 constexpr float kMostOperand = 65504.f;            // fp16's largest value
+// Weights are 2^(score - reference + kWeightBias), the reference raised once a score passes it by kWeightLag.  fp16
+// has 29 binades of normal numbers below 2^15: held there, a weight keeps its 11 bits down to 2^-25 of the
+// reference, and one below that is off by 2^-25 (half a subnormal step), 2^-36 of the reference.  Held around 2^0,
+// 64k weights of 2^-25 beside one dominating token went missing from the product and not from the sum.
+// bf16 has fp32's range and needs no bias.
+template <bool BF16>
+constexpr float kWeightLag = BF16 ? kLazyMax : 4.f;
+template <bool BF16>
+constexpr float kWeightBias = BF16 ? 0.f : 11.f;
 constexpr int kStatusRange = 64;                   // DKV_STATUS_RANGE
 
 struct ChunkParams {
@@ -801,8 +810,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
           for (int e = 1; e < 32; ++e) mx[i] = fmaxf(mx[i], __uint_as_float(s[i][e]));
         }
         const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.qscale;
-        // a higher reference, once some score exceeds the old one by 2^8
-        const bool raise = top > ref + kLazyMax;
+        // a higher reference, once some score exceeds the old one by 2^kWeightLag
+        const bool raise = top > ref + kWeightLag<BF16>;
         if (__any_sync(kFull, raise)) {
           const float now = raise ? top : ref;
           const float a = ex2(ref - now);
@@ -820,7 +829,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             }
           }
         }
-        const float2 sc = f2(p.qscale), off = f2(-ref);
+        const float2 sc = f2(p.qscale), off = f2(kWeightBias<BF16> - ref);
         float2 acc[2] = {f2(0.f), f2(0.f)};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -944,7 +953,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         flush(std::integral_constant<int, D * 4>{}, [&](size_t at) { return p.part_o + (at * p.nsplit + split) * D; });
       if (ok && writes && live && p.nsplit > 1)
         p.part_lse[place_of_row() * p.nsplit + split] =
-            nan ? __int_as_float(0x7fc00000) : (sum == 0.f ? -INFINITY : ref + __log2f(sum));
+            nan ? __int_as_float(0x7fc00000) : (sum == 0.f ? -INFINITY : ref - kWeightBias<BF16> + __log2f(sum));
     }
   }
   tmem_fence_before();
