@@ -437,8 +437,8 @@ __device__ __forceinline__ void mma16816_top(float (&c)[2], const uint32_t (&a)[
   }
 }
 
-// p ~= hi + lo with hi, lo in the 16-bit type of V: returns packed hi pair and lo pair.
-template <bool BF16>
+// p ~= hi + lo / 2^LO with hi, lo in the 16-bit type of V: returns packed hi pair and lo pair.
+template <bool BF16, int LO = 0>
 __device__ __forceinline__ void split_hi_lo(float2 p, uint32_t& hi, uint32_t& lo) {
   if constexpr (BF16) {
     const __nv_bfloat162 h = __floats2bfloat162_rn(p.x, p.y);
@@ -449,7 +449,8 @@ __device__ __forceinline__ void split_hi_lo(float2 p, uint32_t& hi, uint32_t& lo
   } else {
     const __half2 h = __floats2half2_rn(p.x, p.y);
     const float2 hf = __half22float2(h);
-    const __half2 l = __floats2half2_rn(p.x - hf.x, p.y - hf.y);
+    constexpr float k = static_cast<float>(1 << LO);
+    const __half2 l = __floats2half2_rn((p.x - hf.x) * k, (p.y - hf.y) * k);
     hi = *reinterpret_cast<const uint32_t*>(&h);
     lo = *reinterpret_cast<const uint32_t*>(&l);
   }
@@ -707,8 +708,15 @@ __global__ void __launch_bounds__(kThreads) split_kernel(const SplitParams p, co
   static_assert(!(WIN && TMA), "windowed launches read both pools with cp.async");
   // Windowed launches split a weight into three bf16 parts (2^-24; two leave
   // 2^-17, most of the output's error): the third takes the rows 8..11 that the
-  // PV mma has to spare.  fp16's two parts reach 2^-22.
+  // PV mma has to spare.  fp16's two parts reach 2^-22, but fp16 has no numbers
+  // below 2^-24: windowed launches hold the weights 2^7 higher (the lazy
+  // reference lets them grow to 2^15) and the second part, which has rows of its
+  // own, 2^11 higher again, so that a weight is off by at most 2^-43 of the
+  // reference.  Around 2^0, 8192 weights of 2^-25 beside one dominating token
+  // were missing from the output and not from the sum.
   constexpr bool kThree = WIN && BF16;
+  constexpr float kBias = WIN && !BF16 ? 15.f - kLazyMax : 0.f;
+  constexpr int kLoShift = WIN && !BF16 ? 11 : 0;
   constexpr int PPL = D / 16;                  // NeoX pairs per lane
   constexpr int NP2 = PPL / 2;                 // fp32 pairs per half-row per lane
   constexpr int ROW = D * 2;                   // bytes of one token row
@@ -957,6 +965,11 @@ __global__ void __launch_bounds__(kThreads) split_kernel(const SplitParams p, co
         acc[n][0] += acc[n][2];
         acc[n][1] += acc[n][3];
       }
+      if constexpr (kLoShift > 0) {
+        const float k = lane < 16 ? 1.f : 1.f / static_cast<float>(1 << kLoShift);
+        acc[n][0] *= k;
+        acc[n][1] *= k;
+      }
       acc[n][0] += __shfl_xor_sync(kFull, acc[n][0], 16);
       acc[n][1] += __shfl_xor_sync(kFull, acc[n][1], 16);
     }
@@ -971,7 +984,7 @@ __global__ void __launch_bounds__(kThreads) split_kernel(const SplitParams p, co
 #pragma unroll
       for (int n = 0; n < NT; ++n)
         *reinterpret_cast<float2*>(o + 8 * n + 2 * cT) = make_float2(acc[n][0] * inv, acc[n][1] * inv);
-      if (cT == 0) p.part_lse[row] = poisoned ? qnan : (l > 0.f ? M + __log2f(l) : -INFINITY);
+      if (cT == 0) p.part_lse[row] = poisoned ? qnan : (l > 0.f ? M - kBias + __log2f(l) : -INFINITY);
     }
   };
 
@@ -1066,7 +1079,7 @@ __global__ void __launch_bounds__(kThreads) split_kernel(const SplitParams p, co
     float pv[NH];
 #pragma unroll
     for (int k = 0; k < NH; ++k) {
-      pv[k] = ex2(sc[k] - mrun);
+      pv[k] = ex2(sc[k] - (mrun - kBias));
       psum += pv[k];
     }
     if constexpr (G == 4) {
@@ -1090,8 +1103,8 @@ __global__ void __launch_bounds__(kThreads) split_kernel(const SplitParams p, co
       const float2 pa = make_float2(sp[(t0 & 3) * 4 + (t0 >> 2)], sp[((t0 + 1) & 3) * 4 + (t0 >> 2)]);
       const float2 pb = make_float2(sp[(t0 & 3) * 4 + (t0 >> 2) + 2], sp[((t0 + 1) & 3) * 4 + (t0 >> 2) + 2]);
       uint32_t ha, la, hb, lb;
-      split_hi_lo<BF16>(pa, ha, la);
-      split_hi_lo<BF16>(pb, hb, lb);
+      split_hi_lo<BF16, kLoShift>(pa, ha, la);
+      split_hi_lo<BF16, kLoShift>(pb, hb, lb);
       if constexpr (kThree) {
         const float2 fa = widen2<true>(ha), ga = widen2<true>(la), fb = widen2<true>(hb), gb = widen2<true>(lb);
         const __nv_bfloat162 ra = __floats2bfloat162_rn(pa.x - fa.x - ga.x, pa.y - fa.y - ga.y);
