@@ -347,11 +347,19 @@ class PagedKV:
 
     Built from logical K/V bits ``[B, Hkv, Lmax, D]`` with dkv_plan_blocks and
     dkv_pack_kv; the device pool is uploaded once with a torch copy.
+
+    A cache that grows (DecodeAttention.extend) has a table wider than its first lengths need (``stride``) and
+    ``spare_blocks`` more HBM blocks.  ``free_ids`` (device int32) is the stack of the spare blocks' ids and
+    ``free_count`` (device int32 [1]) how many of them are left.  extend changes ``table_dev`` and ``free_count``;
+    the host's ``table``, ``seq_lens`` and ``plan`` stay what the cache was made with.
     """
 
     def __init__(self, k_logical, v_logical, seq_lens, block_size: int, placement: int, host_fraction: float,
-                 shuffle: bool = False, seed: int = 0, stride: int | None = None, device: int = 0):
+                 shuffle: bool = False, seed: int = 0, stride: int | None = None, device: int = 0,
+                 spare_blocks: int = 0):
         import torch
+        if spare_blocks < 0:
+            raise ValueError("spare_blocks must be >= 0")
         B, Hkv, Lmax, D = k_logical.shape
         self.batch, self.num_kv_heads, self.head_dim, self.block_size = B, Hkv, D, block_size
         self.seq_lens = np.ascontiguousarray(seq_lens, dtype=np.int32)
@@ -361,7 +369,7 @@ class PagedKV:
         params = DkvPlanParams(block_size, placement, float(host_fraction), int(shuffle), int(seed))
         self.plan = dkv_plan_blocks(params, self.seq_lens, self.table)
         self.host_split = self.plan.host_split
-        self.num_dev_blocks = self.plan.num_dev_blocks
+        self.num_dev_blocks = self.plan.num_dev_blocks + spare_blocks
         blk = Hkv * block_size * D
         self.k_host = HostPool(self.host_split * blk)
         self.v_host = HostPool(self.host_split * blk)
@@ -375,6 +383,10 @@ class PagedKV:
         del k_stage, v_stage
         self.table_dev = torch.from_numpy(self.table).to(dev)
         self.seq_lens_dev = torch.from_numpy(self.seq_lens).to(dev)
+        first_spare = self.host_split + self.plan.num_dev_blocks
+        # the top of the stack, its last entry, is the lowest id
+        self.free_ids = torch.arange(first_spare + spare_blocks - 1, first_spare - 1, -1, dtype=torch.int32, device=dev)
+        self.free_count = torch.tensor([spare_blocks], dtype=torch.int32, device=dev)
 
     @property
     def host_bytes(self) -> int:
