@@ -3,8 +3,9 @@
 Argument marshalling only.  Every step of the decode path runs in the CUDA
 kernels of ``libdkv.so`` (built in-tree by ``python
 decode_attention_host_b200/build.py``); importing this package fails loudly if
-the library is missing, and there is no CPU fallback.  PyTorch is used for
-device memory and streams.
+the library is missing, and there is no CPU fallback.  ``_dkv_call``, a small
+CPython module, makes the serving step's calls where it is built for this
+Python; elsewhere ctypes does.  PyTorch is used for device memory and streams.
 
 The functions ``dkv_*`` mirror the C ABI in ``include/dkv.h`` one to one and
 raise :class:`DkvError` when the C call returns a nonzero code.  The classes
@@ -15,6 +16,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import operator
 import os
 from pathlib import Path
 
@@ -123,13 +125,6 @@ def _load() -> ctypes.CDLL:
 
 lib = _load()
 
-try:
-    from . import _dkv_call
-except ImportError as e:
-    raise ImportError("_dkv_call.so is missing: build it with `python decode_attention_host_b200/build.py`") from e
-_dkv_call.load(str(LIB_PATH))
-
-
 def _check(rc: int) -> None:
     if rc != DKV_OK:
         raise DkvError(rc, lib.dkv_last_error_string().decode())
@@ -144,6 +139,38 @@ def _p(x) -> int | None:
     if isinstance(x, np.ndarray):
         return x.ctypes.data
     return x.data_ptr()
+
+
+class _CtypesCalls:
+    """What _dkv_call offers, through the library's ctypes signatures: 3 us more for each call.  Its checks are the
+    same: the number of arguments, and whole numbers that fit their C type, which ctypes would cut off."""
+
+    def __init__(self):
+        for name in ("extend_tables", "store_kv", "attn_chunk", "attn_decode_window"):
+            setattr(self, name, self._bind(getattr(lib, "dkv_" + name)))
+
+    @staticmethod
+    def _bind(fn):
+        def number(x, bits):
+            x = operator.index(x)
+            if not -(1 << (bits - 1)) <= x < 1 << (bits - 1):
+                raise OverflowError("argument does not fit its C type")
+            return x
+
+        kinds = [0 if t is ctypes.c_void_p else 8 * ctypes.sizeof(t) for t in fn.argtypes]
+
+        def call(*args):
+            if len(args) != len(kinds):
+                raise TypeError(f"{len(kinds)} arguments are needed, {len(args)} were given")
+            return fn(*[number(x, k) if k else _p(x) for x, k in zip(args, kinds)])
+        return call
+
+
+try:
+    from . import _dkv_call
+    _dkv_call.load(str(LIB_PATH))
+except ImportError:     # not built for this Python
+    _dkv_call = _CtypesCalls()
 
 
 # ----------------------------------------------------------------------------- C ABI, one to one
@@ -186,8 +213,8 @@ def dkv_attn_decode_multi(h, num_queries, q, k_host, v_host, k_dev, v_dev, block
                                      int(block_table_stride), int(num_dev_blocks)))
 
 
-# The entry points of a serving step go through _dkv_call, which reads the arguments without ctypes: addresses may
-# be tensors, whole numbers or None.
+# The entry points of a serving step go through _dkv_call, which reads the arguments without ctypes where it is built:
+# addresses may be tensors, whole numbers or None.
 
 def dkv_extend_tables(h, seq_lens, new_lens, batch, block_table, block_table_stride, free_ids, free_capacity,
                       free_count, free_left, q_start, slot_map, max_slots, stream) -> None:

@@ -20,7 +20,8 @@ SOURCES = [CSRC / "dkv_api.cu", CSRC / "dkv_noalloc.cu", CSRC / "dkv_serve.cu", 
 HEADERS = [CSRC / "dkv_kernels.cuh", CSRC / "dkv_append.cuh", CSRC / "dkv_multi.cuh", CSRC / "dkv_chunk.cuh",
            CSRC / "dkv_tables.cuh", CSRC / "dkv_handle.h", CSRC / "dkv_error.h", CSRC / "dkv_plan.h",
            CSRC / "dkv_tma.h", ROOT / "include" / "dkv.h"]
-CALL_LIB = PKG / "_dkv_call.so"
+# named with this Python's ABI tag, so that another Python never loads it
+CALL_LIB = PKG / ("_dkv_call" + sysconfig.get_config_var("EXT_SUFFIX"))
 CALL_SOURCE = CSRC / "dkv_python.cpp"
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 FLAGS = ["-O3", "-std=c++17", "-gencode", "arch=compute_100a,code=sm_100a", "-lineinfo",
@@ -29,14 +30,16 @@ FLAGS = ["-O3", "-std=c++17", "-gencode", "arch=compute_100a,code=sm_100a", "-li
 
 
 def up_to_date() -> bool:
-    if not LIB.exists() or not CALL_LIB.exists():
-        return False
-    t = min(LIB.stat().st_mtime, CALL_LIB.stat().st_mtime)
-    return all(p.stat().st_mtime <= t for p in SOURCES + HEADERS + [CALL_SOURCE, Path(__file__)])
+    return LIB.exists() and all(p.stat().st_mtime <= LIB.stat().st_mtime for p in SOURCES + HEADERS + [Path(__file__)])
 
 
-def build_calls(force: bool = False) -> Path:
-    """Compile the CPython calls (host code only; they open libdkv.so at import)."""
+def build_calls(force: bool = False) -> Path | None:
+    """Compile the CPython calls (host code only; they open libdkv.so at import).  Without Python's headers there are
+    none, and the package makes the same calls through ctypes."""
+    (PKG / "_dkv_call.so").unlink(missing_ok=True)   # an untagged build, which any Python would load
+    if not (Path(sysconfig.get_paths()["include"]) / "Python.h").exists():
+        print("no Python.h: the serving step's calls go through ctypes", file=sys.stderr)
+        return None
     newest = max(p.stat().st_mtime for p in (CALL_SOURCE, ROOT / "include" / "dkv.h", Path(__file__)))
     if force or not CALL_LIB.exists() or CALL_LIB.stat().st_mtime < newest:
         tmp = CALL_LIB.with_suffix(f".{os.getpid()}.tmp.so")
@@ -51,6 +54,7 @@ def build(force: bool = False, verbose: bool = False, out: Path = LIB, defines: 
     """Compile the library to ``out``; ``defines`` are extra -D build-time knobs (e.g. DKV_DEV_STAGES=2)."""
     out = Path(out)
     if not force and not defines and out == LIB and up_to_date():
+        build_calls()
         return LIB
     tmp = out.with_suffix(f".{os.getpid()}.tmp.so")
     cmd = [NVCC, *FLAGS, *(f"-D{d}" for d in defines), *(["-Xptxas", "-v"] if verbose else []), "-o", str(tmp),
