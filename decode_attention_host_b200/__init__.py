@@ -543,8 +543,8 @@ class DecodeAttention:
 
     def chunk(self, q, q_start, kv: PagedKV, out, window: int = 0, sinks: int = 0, include_self: bool = True,
               k_stage=None, v_stage=None, stream=None) -> None:
-        """q, out [rows, Hq, D] (of the handle's type): rows q_start[b] .. q_start[b+1] are the new tokens of sequence b,
-        at positions seq_lens[b] ..; causal over the cache, under a window of tokens and sinks if window > 0."""
+        """q, out [rows, Hq, D] of the handle's type: rows q_start[b] .. q_start[b+1] are the new tokens of sequence b, at
+        positions seq_lens[b] ..; causal over the cache, under a window of tokens and sinks if window > 0."""
         import torch
         hq, d = self.cfg.num_q_heads, self.cfg.head_dim
         rows = q.shape[0]

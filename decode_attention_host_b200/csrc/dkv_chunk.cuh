@@ -40,8 +40,9 @@
 // cache types (fp32 rotation, one rounding to 2^-11; bf16 operands would be
 // off by 2^-8, the largest error of the whole computation), unrotated ones as
 // stored; the weights P take V's type, as one instruction multiplies equal
-// types.  Everything else is fp32.  A rotated component beyond fp16's range
-// poisons the rows that see it and sets a status bit.
+// types.  Everything else is fp32.  A rotated component beyond fp16's range, or
+// a block id outside the pools, makes the rows that see it NaN (the kernel
+// notes the first and the last such token of a CTA) and sets a status bit.
 #pragma once
 
 #include <type_traits>
@@ -61,7 +62,7 @@ constexpr int kRegsIssue = 64;
 constexpr int kRegsRotate = 96;
 constexpr int kRegsSoftmax = 176;
 static_assert(kRegsIssue + kRegsRotate + 2 * kRegsSoftmax <= 4 * kRegsLaunch, "setmaxnreg.inc would wait for ever");
-constexpr float kMostOperand = 65504.f;            // fp16's largest value
+constexpr float kMostOperand = 65504.f;            // fp16's largest value; what rounds to it is in range too
 // Weights are 2^(score - reference + kWeightBias), the reference raised once a score passes it by kWeightLag.  fp16
 // has 29 binades of normal numbers below 2^15: held there, a weight keeps its 11 bits down to 2^-25 of the
 // reference, and one below that is off by 2^-25 (half a subnormal step), 2^-36 of the reference.  Held around 2^0,
@@ -118,7 +119,8 @@ struct ChunkTail {
   uint32_t tmem;
   int32_t b, tile;                             // the CTA's sequence (-1: none) and row tile
   int32_t q0, n, len;                          // its first row, rows and cached tokens
-  int32_t poison;                              // an invalid block id or an operand out of range
+  int32_t bad_lo, bad_hi;                      // first and last token of an invalid block or with a key out of range
+  uint32_t bad_rows[8];                        // a query out of range, by softmax warp and lane
   int32_t broken;                              // a wait ran out: every role gives up
 };
 
@@ -362,7 +364,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       t.q0 = fq;
       t.n = fn;
       t.len = fl;
-      t.poison = 0;
+      t.bad_lo = INT32_MAX;
+      t.bad_hi = -1;
+      for (int i = 0; i < 8; ++i) t.bad_rows[i] = 0;
       t.broken = 0;
     }
   } else if (warp == 1 && lane == 0) {
@@ -474,8 +478,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
           const int t0 = tile_pos(j) + lane * p.box;
           host = id < p.host_split;
           y = ((host ? id : id - p.host_split) * p.hkv + h) * p.block_size + (t0 - p.div_bs.div(t0) * p.block_size);
-        } else if (id != -2) {
-          *reinterpret_cast<volatile int32_t*>(&t.poison) = 1;
+        } else if (id != -2) {   // the run's tokens that some row sees
+          const int t0 = tile_pos(j) + lane * p.box, t1 = t0 + p.box;
+          atomicMin(&t.bad_lo, t0 < sk_end ? t0 : max(t0, lo_min));
+          atomicMax(&t.bad_hi, (t1 > lo_min ? min(t1, hi_max) : min(t1, sk_end)) - 1);
           atomicOr(p.status, 1);
         }
         __syncwarp();
@@ -688,9 +694,21 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
           *px = make_uint4(o[0], o[1], o[2], o[3]);
           *py = make_uint4(o[4], o[5], o[6], o[7]);
         }
-        if (mx > kMostOperand) {
-          *reinterpret_cast<volatile int32_t*>(&t.poison) = 1;
-          atomicOr(p.status, kStatusRange);
+        if (mx > kMostOperand) {   // rare: which of this thread's rows hold an infinity now
+#pragma unroll 1
+          for (int rw = rr; rw < kChunkTokens; rw += kStep) {
+            const int tt = p0 + rw;
+            if (tt >= hi_max || (tt < lo_min && tt >= sk_end)) continue;
+            const char* const at = k + rw * 128;
+            const uint4 ux = *reinterpret_cast<const uint4*>(at + ((c ^ (rw & 7)) << 4));
+            const uint4 uy = D == 128 ? *reinterpret_cast<const uint4*>(at + kSubTile + ((c ^ (rw & 7)) << 4))
+                                      : *reinterpret_cast<const uint4*>(at + (((c + 4) ^ (rw & 7)) << 4));
+            const uint32_t mu = hmax_abs2(hmax_abs2(hmax_abs2(hmax_abs2(0u, ux.x), ux.y), ux.z), ux.w);
+            if (!has_inf2(hmax_abs2(hmax_abs2(hmax_abs2(hmax_abs2(mu, uy.x), uy.y), uy.z), uy.w))) continue;
+            atomicMin(&t.bad_lo, tt);
+            atomicMax(&t.bad_hi, tt);
+            atomicOr(p.status, kStatusRange);
+          }
         }
       }
       fence_proxy_async();   // the products read what was written here
@@ -735,7 +753,6 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             turn_cs(step, t1, E[i].y, F[i].y);
           }
         }
-        uint32_t mx = 0;
         char* const dst = sq + m * C::kTile;
 #pragma unroll
         for (int i = 0; i < kC; ++i) {
@@ -744,12 +761,19 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             float2 X[4] = {widen2<BF16>(ux[i].x), widen2<BF16>(ux[i].y), widen2<BF16>(ux[i].z), widen2<BF16>(ux[i].w)};
             float2 Y[4] = {widen2<BF16>(uy[i].x), widen2<BF16>(uy[i].y), widen2<BF16>(uy[i].z), widen2<BF16>(uy[i].w)};
             rope_rotate_advance<4>(X, Y, Cc, Sc, E, F);
-            uint32_t o[8];
+            uint32_t o[8], mx = 0;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               o[e] = narrow2<false>(X[e].x, X[e].y);
               o[4 + e] = narrow2<false>(Y[e].x, Y[e].y);
               mx = hmax_abs2(hmax_abs2(mx, o[e]), o[4 + e]);
+            }
+            // lanes [kC g, kC (g + 1)) hold row kPer i + g of the warp's 32; in shared
+            // memory, as a register held over the walk cost 3% with few rows
+            const unsigned inf = __ballot_sync(kFull, has_inf2(mx));
+            if (inf && lane / kPer == i && (inf >> (kC * (lane % kPer)) & ((1u << kC) - 1u)) != 0) {
+              atomicOr(&t.bad_rows[warp - 8], 1u << lane);
+              atomicOr(p.status, kStatusRange);
             }
             ux[i] = make_uint4(o[0], o[1], o[2], o[3]);
             uy[i] = make_uint4(o[4], o[5], o[6], o[7]);
@@ -757,10 +781,6 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
           *reinterpret_cast<uint4*>(dst + r * 128 + ((c ^ (r & 7)) << 4)) = ux[i];
           if constexpr (D == 128) *reinterpret_cast<uint4*>(dst + kSubTile + r * 128 + ((c ^ (r & 7)) << 4)) = uy[i];
           else *reinterpret_cast<uint4*>(dst + r * 128 + (((c + 4) ^ (r & 7)) << 4)) = uy[i];
-        }
-        if (has_inf2(mx)) {
-          *reinterpret_cast<volatile int32_t*>(&t.poison) = 1;
-          atomicOr(p.status, kStatusRange);
         }
         fence_proxy_async();
         __syncwarp();
@@ -892,7 +912,11 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         }
       }
       ok = ok && *reinterpret_cast<volatile int32_t*>(&t.broken) == 0;
-      const bool nan = !ok || *reinterpret_cast<volatile int32_t*>(&t.poison);
+      // NaN: the row sees an invalid token (of several, the first and the last are known)
+      const int bad_lo = *reinterpret_cast<volatile int32_t*>(&t.bad_lo);
+      const int bad_hi = *reinterpret_cast<volatile int32_t*>(&t.bad_hi);
+      const uint32_t bad_rows = *reinterpret_cast<volatile uint32_t*>(&t.bad_rows[warp - 8]);
+      const bool nan = !ok || (bad_rows >> lane & 1u) || (hi > bad_lo && (lo <= bad_hi || bad_lo < p.sinks));
       const float inv = nan ? __int_as_float(0x7fc00000) : (sum == 0.f ? 0.f : 1.f / sum);
       auto flush = [&](auto bytes, auto&& place) {   // the warp's 32 rows of `bytes` bytes to place(row of the warp)
         constexpr int kRow = decltype(bytes)::value, kC = kRow / 16, kPer = 32 / kC;

@@ -58,7 +58,8 @@ extern "C" {
 #define DKV_STATUS_INTERNAL 8     /* the HBM kernel found its shared memory misaligned and did nothing */
 #define DKV_STATUS_NO_FREE_BLOCKS 16 /* dkv_extend_tables: the free list holds too few blocks (nothing was changed) */
 #define DKV_STATUS_NO_SLOTS 32    /* dkv_extend_tables: more new tokens than max_slots (nothing was changed) */
-#define DKV_STATUS_RANGE 64       /* dkv_attn_chunk: a rotated query or key component above 65504; rows that may see it are NaN */
+#define DKV_STATUS_RANGE 64       /* dkv_attn_chunk: a rotated query or key component beyond 65504; the
+                                     query's row, and the rows that see the key, are NaN */
 
 typedef enum { DKV_KV_F16 = 0, DKV_KV_BF16 = 1 } dkv_kv_dtype;
 
@@ -289,11 +290,17 @@ DKV_API int dkv_store_kv(dkv_handle* h, const void* k_new, const void* v_new, in
  *                 them the first host_split blocks of the host pools are
  *                 copied there first.
  * Scores, softmax statistics and outputs are accumulated in fp32; rotated
- * queries and keys are held in fp16 (|x| <= 65504 after rotation, else
- * DKV_STATUS_RANGE and NaN for the 256 / (Hq/Hkv) rows of the chunk that are
- * computed together), softmax weights in the handle's kv_dtype.  A V row that
- * is not finite spoils the rows that see it, and rows computed together with
- * those.
+ * queries and keys are held in fp16 (without rotation as stored), softmax
+ * weights in the handle's kv_dtype, each rounded once: of normally distributed
+ * inputs an fp16 output is off by 4.1e-4 of its norm (2.1e-4 is its own
+ * rounding), a bf16 one by 2.4e-3 (1.7e-3).  A rotated component beyond 65504
+ * sets DKV_STATUS_RANGE: its query's row and head, and the rows that see its
+ * key, are NaN.  A block id outside both pools sets DKV_STATUS_BAD_BLOCK_ID,
+ * and the rows that see a token of the block are NaN.  (Under a window, rows
+ * between two such tokens that see neither may be NaN too.)  A V row that is
+ * not finite spoils the rows that see it, and other rows of its sequence that
+ * are computed together with those: 128 or 256 / (Hq/Hkv) rows, by the call's
+ * rows per sequence.
  * Errors: INVALID_ARG, CUDA. */
 DKV_API int dkv_attn_chunk(dkv_handle* h, const void* q, int64_t q_stride, const int32_t* q_start,
                            int32_t total_rows, const void* k_host, const void* v_host, const void* k_dev,
