@@ -29,6 +29,12 @@ constexpr int kWinHostUnits = 4;
 
 bool misaligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) != 0; }
 
+// Whether one of the arrays of 4-byte numbers could not be loaded from.
+template <class... P>
+bool misaligned4(P... p) {
+  return (misaligned(p, 4) || ...);
+}
+
 template <int D, int G, bool BF16, bool ROPE>
 void launch_window(dim3 grid, size_t smem, cudaStream_t s, const dkv::SplitParams& p, const dkv::TileMaps& m) {
   dkv::split_kernel<D, G, BF16, kWinStages, ROPE, false, true><<<grid, dkv::kThreads, smem, s>>>(p, m);
@@ -210,6 +216,8 @@ int dkv_extend_tables(dkv_handle* h, const int32_t* seq_lens, const int32_t* new
     return set_error(DKV_ERR_INVALID_ARG, "dkv_extend_tables: stride, free_capacity or max_slots out of range");
   if (misaligned(slot_map, 8))
     return set_error(DKV_ERR_INVALID_ARG, "dkv_extend_tables: slot_map must be 8-byte aligned");
+  if (misaligned4(seq_lens, new_lens, block_table, free_ids, free_count, free_left, q_start))
+    return set_error(DKV_ERR_INVALID_ARG, "dkv_extend_tables: the int32 arrays must be 4-byte aligned");
   dkv::DeviceGuard guard(c.device);
   if (!guard.ok) return set_error(DKV_ERR_CUDA, "cudaSetDevice failed");
   dkv::TableParams p{};
@@ -311,6 +319,8 @@ int dkv_attn_chunk(dkv_handle* h, const void* q, int64_t q_stride, const int32_t
     return set_error(DKV_ERR_INVALID_ARG, "dkv_attn_chunk: q_stride must be a multiple of 8, at least Hq * D");
   if (misaligned(q, 16) || misaligned(out, 16))
     return set_error(DKV_ERR_INVALID_ARG, "dkv_attn_chunk: q and out must be 16-byte aligned");
+  if (misaligned4(q_start, block_table, seq_lens))
+    return set_error(DKV_ERR_INVALID_ARG, "dkv_attn_chunk: q_start, the table and seq_lens must be 4-byte aligned");
   const bool staged = k_stage != nullptr || v_stage != nullptr;
   if (staged && (!k_stage || !v_stage || misaligned(k_stage, 16) || misaligned(v_stage, 16)))
     return set_error(DKV_ERR_INVALID_ARG, "dkv_attn_chunk: staging pools must both be given, 16-byte aligned");
@@ -423,6 +433,8 @@ int dkv_attn_decode_window(dkv_handle* h, int32_t window, int32_t sinks, int32_t
   if (block_table_stride < 1)
     return set_error(DKV_ERR_INVALID_ARG, "dkv_attn_decode_window: block_table_stride must be >= 1");
   if (misaligned(q, 8)) return set_error(DKV_ERR_INVALID_ARG, "dkv_attn_decode_window: q must be 8-byte aligned");
+  if (misaligned4(out, block_table, seq_lens))
+    return set_error(DKV_ERR_INVALID_ARG, "dkv_attn_decode_window: out, the table and seq_lens must be 4-byte aligned");
   dkv::DeviceGuard guard(c.device);
   if (!guard.ok) return set_error(DKV_ERR_CUDA, "cudaSetDevice failed");
   if ((rc = check_cache(h, "dkv_attn_decode_window", k_host, v_host, k_dev, v_dev, host_split, num_dev_blocks)) !=

@@ -208,7 +208,8 @@ DKV_API int dkv_append_kv(dkv_handle* h, const float* x, const void* w_k, const 
  * synchronise, and may be captured into a CUDA graph; lengths, tables and the
  * free list are read on the device, so a captured step follows them.  Like
  * dkv_attn_decode they use the handle's workspace: one call at a time per
- * handle.  Block ids and pools are those of dkv_attn_decode. */
+ * handle.  Block ids and pools are those of dkv_attn_decode.  Arrays of 4-byte
+ * numbers must be 4-byte aligned (INVALID_ARG). */
 
 /*
  * dkv_extend_tables -- grow the block tables by this step's new tokens and
