@@ -28,13 +28,16 @@
 //               rarely), P goes back to TMEM over the S it came from
 // A chunk of at most 128 rows a kv head takes CTAs of 128 rows (DUAL, below).
 //
-// Measured on a B200, 32 query heads over 8 kv heads, D = 128, bf16: 2048 rows on
-// 30720 tokens in 1.08 ms, 0.99 PFLOP/s (0.6 of a plain matrix product; without
-// rotation 0.89 ms, 1.2 PFLOP/s); 8 rows on four 64k contexts in 202 us, 5.3 TB/s.
-// A K/V tile takes about 3900 cycles where its products take 2100: the softmax
-// warps and the rotating one share the schedulers, 47% of whose slots issue, and
-// the tensor core waits for P.  The 128 x 128 tiles are what TMEM's 512 columns
-// hold twice (S and O); N = 64 halves the products' rate.
+// Measured on a B200, 32 query heads over 8 kv heads, D = 128, bf16, in a burst
+// and in a loop at lower clocks: 2048 rows on 30720 tokens in 1.08 and 1.23 ms,
+// 0.99 and 0.87 PFLOP/s (0.6 of a plain matrix product; without rotation 0.89
+// ms, 1.2 PFLOP/s); 8 rows on four 64k contexts in 202 and 246 us, 5.3 and 4.4
+// TB/s.  A K/V tile takes about 3900 cycles where its products take 2100: the
+// softmax warps and the rotating one share the schedulers, 47% of whose slots
+// issue, and the tensor core waits for P.  The long case's 256 CTAs are 1.73
+// waves of 148 SMs and take two; its rows are too many for the workspace that
+// splits need.  The 128 x 128 tiles are what TMEM's 512 columns hold twice (S
+// and O); N = 64 halves the products' rate.
 //
 // Roundings to 16 bits: rotated queries and keys are held in fp16 for both
 // cache types (fp32 rotation, one rounding to 2^-11; bf16 operands would be
