@@ -157,12 +157,15 @@ class _CtypesCalls:
                 raise OverflowError("argument does not fit its C type")
             return x
 
+        def address(x):
+            return x if x is None or isinstance(x, int) else x.data_ptr()
+
         kinds = [0 if t is ctypes.c_void_p else 8 * ctypes.sizeof(t) for t in fn.argtypes]
 
         def call(*args):
             if len(args) != len(kinds):
                 raise TypeError(f"{len(kinds)} arguments are needed, {len(args)} were given")
-            return fn(*[number(x, k) if k else _p(x) for x, k in zip(args, kinds)])
+            return fn(*[number(x, k) if k else address(x) for x, k in zip(args, kinds)])
         return call
 
 

@@ -6,6 +6,7 @@ import sys
 import sysconfig
 from pathlib import Path
 
+import numpy as np
 import pytest
 
 import decode_attention_host_b200 as dkv
@@ -62,3 +63,11 @@ def test_both_ways_refuse_alike(name, n):
                            (None, TypeError)):
             with pytest.raises(error):
                 f(*args[:number], bad, *args[number + 1:])
+
+
+def test_both_ways_take_no_host_array_for_an_address():
+    """A numpy array lies in host memory: the kernels would read its address."""
+    args = [None if t is ctypes.c_void_p else 0 for t in dkv.lib.dkv_store_kv.argtypes]
+    for way in ways():
+        with pytest.raises(AttributeError):
+            way.store_kv(args[0], np.zeros(4), *args[2:])
