@@ -125,6 +125,7 @@ def _load() -> ctypes.CDLL:
 
 lib = _load()
 
+
 def _check(rc: int) -> None:
     if rc != DKV_OK:
         raise DkvError(rc, lib.dkv_last_error_string().decode())
