@@ -131,6 +131,9 @@ DKV_API int dkv_destroy(dkv_handle* h);
  * is launched.  Table entries outside both pools and out-of-range lengths are
  * detected on the device: the status word records DKV_STATUS_* bits and the
  * affected rows of out are written as NaN (there is no device trap).
+ * With an fp16 cache a softmax weight counts in steps of 2^-24 of its split's
+ * largest: weights below half of that are missing from the sum of values
+ * (dkv_attn_decode_window and dkv_attn_chunk keep them).
  */
 DKV_API int dkv_attn_decode(dkv_handle* h, const float* q, const void* k_host, const void* v_host,
                     const void* k_dev, const void* v_dev, const int32_t* block_table,
